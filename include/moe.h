@@ -72,6 +72,8 @@ typedef enum {
 #define MOE_DEV_BAD_EXPERT_ID        0x4u   /* a routed expert index outside [0, E) */
 #define MOE_DEV_WAIT_TIMEOUT_ROUTER  0x8u   /* a bounded wait expired in the router GEMM */
 #define MOE_DEV_WAIT_TIMEOUT_SEND    0x10u  /* a sender gave up waiting for a group's tiles */
+#define MOE_DEV_WAIT_TIMEOUT_FEW     0x20u  /* a bounded wait expired in moe_forward_few */
+#define MOE_DEV_WAIT_TIMEOUT_PRODUCT 0x40u  /* a bounded wait expired in a block-scaled product */
 
 /* Shape of the layer; fixed for the lifetime of a plan. */
 typedef struct {
@@ -174,6 +176,93 @@ typedef struct {
 moe_status moe_forward(moe_plan_t plan, const moe_weights *weights, const void *hidden,
                        const uint8_t *valid, int T, int k, void *out, void *workspace,
                        size_t ws_bytes, void *stream, moe_debug *dbg);
+
+/* moe_forward for a few tokens, T <= MOE_FEW_TOKENS_MAX, in one kernel: router, top-k,
+ * gate/up, SwiGLU, down and combine without a launch between them (Step3 推論最適化
+ * (MI308X vs H20), §最適化技術: the one-stage MoE kernel).  For so few tokens the layer is
+ * one read of the selected experts' weights; the same layer, arguments, weights and
+ * workspace as moe_forward, with the same rules for ties, padding rows and rounding, so
+ * the two agree to the rounding of their sums (which they take in other orders; bf16
+ * weights: h enters the down product with about fp32's precision in both; FP8: the y of
+ * an expert is not rounded to bf16 before the combine here).  Each expert weight is read
+ * once per call whatever the number of tokens that selected it; experts that no token
+ * selected are not read.
+ *
+ * Differences from moe_forward: router_w is read as it is (router_split is not used);
+ * T > MOE_FEW_TOKENS_MAX returns MOE_ERR_UNSUPPORTED; of dbg, logits, topk_ids and topk_w
+ * are filled and events[0] and events[MOE_NUM_STAGES] recorded before and after, while
+ * perm or offsets that are not NULL return MOE_ERR_UNSUPPORTED (there is no permutation).
+ * The kernel is a cooperative launch over all SMs whose CTAs wait for one another (each
+ * wait bounded by the plan's wait limit, MOE_DEV_WAIT_TIMEOUT_FEW): on a device shared
+ * with long-running kernels of other streams it starts when they have left the SMs. */
+#define MOE_FEW_TOKENS_MAX 16
+moe_status moe_forward_few(moe_plan_t plan, const moe_weights *weights, const void *hidden,
+                           const uint8_t *valid, int T, int k, void *out, void *workspace,
+                           size_t ws_bytes, void *stream, moe_debug *dbg);
+
+/* ------------------------------------------------- dense layers in the FP8 weight format
+ *
+ * The FP8 layer's arithmetic (e4m3 weights with an fp32 scale per 128x128 block, e4m3
+ * activations with an fp32 scale per 1x128 group) for a model's dense layers: quantise the
+ * activations, multiply.  A dense gate/up/down MLP is quantise, product, gated quantise,
+ * product. */
+
+typedef enum {
+    MOE_T_BF16 = 0,
+    MOE_T_FP32 = 1
+} moe_dtype;
+
+/* Activation quantisation.  Row r of x (bf16 or fp32, device) starts at x + r * ldx
+ * elements and holds cols values v, or with gated = 1 cols values g and then cols values u,
+ * and v = silu(g) * u in fp32.  For every group of 128 consecutive columns (the last one
+ * may be shorter):
+ *   scales[r, group] = amax / 448 over the group's |v| (fp32; 1 where amax = 0)
+ *   codes[r, c]      = the e4m3 value nearest v / scale (fp32 division, ties to even)
+ * codes: e4m3 bytes [rows, cols], scales: fp32 [rows, ceil(cols / 128)], both dense.  Rows
+ * with valid[r] = 0 (valid: uint8 [rows] or NULL) are padding: their contents are not read,
+ * their codes are 0 and their scales 1, so a product with them gives zero rows.  A NaN
+ * gives NaN codes where it stands and is left out of its group's amax; an infinite
+ * amax gives code 0 to the group's finite values and NaN to the infinite ones.
+ * cols is a multiple of 16 (else MOE_ERR_UNSUPPORTED); ldx >= cols * (1 + gated), with rows
+ * of x and codes 16-byte aligned (ldx a multiple of 8 for bf16, of 4 for fp32).
+ * Needs no workspace; x must not overlap codes or scales. */
+moe_status moe_quantize_groups(const void *x, moe_dtype x_type, int rows, int cols, int64_t ldx,
+                               int gated, const uint8_t *valid, void *codes, float *scales,
+                               void *stream);
+
+/* Block-scaled product out = A W^T:
+ *   out[m, n] = sum_kb a_scales[m, kb] * w_scales[n / 128, kb]
+ *                      * sum_{k in block kb} A[m, k] * W[n, k]
+ * with exact products of the e4m3 codes, fp32 sums, and one rounding to out_type.
+ * A: [rows, k] with a_scales [rows, ceil(k / 128)]; W: [n, k] with w_scales
+ * [ceil(n / 128), ceil(k / 128)]; all dense, device; A and W 16-byte aligned.  Row m of
+ * out (bf16 or fp32) starts at out + m * ldo elements, ldo >= n; only its n values are
+ * written.  Any rows and n; k a multiple of 16 (else MOE_ERR_UNSUPPORTED).
+ *
+ * A moe_product holds the shape and its workspace size, as a plan does for the layer:
+ * moe_product_create touches no device; one workspace (256-byte aligned, at least
+ * *workspace_bytes) serves one product at a time; rows 0..max_rows.  Device waits are
+ * bounded (moe_product_set_wait_limit, nanoseconds, default 2e9) and report
+ * MOE_DEV_WAIT_TIMEOUT_PRODUCT through moe_product_device_status, which synchronises the
+ * stream and reads and clears the status word of this workspace, like
+ * moe_check_device_status.  Make the first product on a device outside graph capture. */
+typedef struct {
+    int max_rows;       /* largest number of rows of A, 1..2^24 */
+    int n;              /* rows of W, 1..2^24 */
+    int k;              /* multiple of 16, at most 2^20 */
+    moe_dtype out_type;
+} moe_product_config;
+typedef struct moe_product_s *moe_product_t;
+
+moe_status moe_product_create(const moe_product_config *cfg, moe_product_t *product,
+                              size_t *workspace_bytes);
+void moe_product_destroy(moe_product_t product);
+moe_status moe_product_set_wait_limit(moe_product_t product, uint64_t limit_ns);
+moe_status moe_block_scaled_product(moe_product_t product, const void *a, const float *a_scales,
+                                    const void *w, const float *w_scales, int rows, void *out,
+                                    int64_t ldo, void *workspace, size_t ws_bytes, void *stream);
+moe_status moe_product_device_status(moe_product_t product, void *workspace, void *stream,
+                                     uint32_t *bits);
 
 /* Tensor-parallel MoE (DP Attention and TBO for DeepSeek-V4 on MI355X,
  * introduction: DP attention in front of a TP MoE joined by all_gather /

@@ -28,6 +28,13 @@ MOE_DEV_WAIT_TIMEOUT_DOWN = 0x2
 MOE_DEV_BAD_EXPERT_ID = 0x4
 MOE_DEV_WAIT_TIMEOUT_ROUTER = 0x8
 MOE_DEV_WAIT_TIMEOUT_SEND = 0x10
+MOE_DEV_WAIT_TIMEOUT_FEW = 0x20
+MOE_DEV_WAIT_TIMEOUT_PRODUCT = 0x40
+
+MOE_T_BF16 = 0
+MOE_T_FP32 = 1
+
+MOE_FEW_TOKENS_MAX = 16
 
 MOE_NUM_STAGES = 7
 STAGE_NAMES = ("router", "topk", "permute", "gather", "gate_up_gemm", "down_gemm", "combine")
@@ -39,7 +46,9 @@ EXPORTED = ("moe_plan_create", "moe_plan_destroy", "moe_plan_set_wait_limit", "m
             "moe_pipeline_slot_bytes", "moe_pipeline_create", "moe_pipeline_submit",
             "moe_pipeline_synchronize", "moe_pipeline_streams", "moe_pipeline_destroy",
             "moe_router_split_bytes", "moe_split_router_weights", "moe_forward_scatter_pairs",
-            "moe_reduce_pairs")
+            "moe_reduce_pairs", "moe_forward_few", "moe_quantize_groups", "moe_product_create",
+            "moe_product_destroy", "moe_product_set_wait_limit", "moe_block_scaled_product",
+            "moe_product_device_status")
 MAX_TP_RANKS = 8
 
 MOE_STATIC_SCRATCH_BYTES = 4 << 20
@@ -69,6 +78,10 @@ class moe_workspace_views(ctypes.Structure):
     _fields_ = [("row_token", _vp), ("x_perm", _vp), ("h", _vp), ("y", _vp),
                 ("group_offsets", _vp), ("h_stride", _c_int), ("x_scale", _vp),
                 ("h_scale", _vp)]
+
+
+class moe_product_config(ctypes.Structure):
+    _fields_ = [("max_rows", _c_int), ("n", _c_int), ("k", _c_int), ("out_type", _c_int)]
 
 
 class MoeError(RuntimeError):
@@ -147,6 +160,24 @@ def load():
     L.moe_router_split_bytes.restype = ctypes.c_size_t
     L.moe_split_router_weights.argtypes = [_vp, _vp, _vp, ctypes.c_size_t, _vp]
     L.moe_split_router_weights.restype = _c_int
+    L.moe_forward_few.argtypes = [_vp, ctypes.POINTER(moe_weights), _vp, _vp, _c_int, _c_int, _vp,
+                                  _vp, ctypes.c_size_t, _vp, ctypes.POINTER(moe_debug)]
+    L.moe_forward_few.restype = _c_int
+    L.moe_quantize_groups.argtypes = [_vp, _c_int, _c_int, _c_int, ctypes.c_int64, _c_int, _vp,
+                                      _vp, _vp, _vp]
+    L.moe_quantize_groups.restype = _c_int
+    L.moe_product_create.argtypes = [ctypes.POINTER(moe_product_config), ctypes.POINTER(_vp),
+                                     ctypes.POINTER(ctypes.c_size_t)]
+    L.moe_product_create.restype = _c_int
+    L.moe_product_destroy.argtypes = [_vp]
+    L.moe_product_destroy.restype = None
+    L.moe_product_set_wait_limit.argtypes = [_vp, ctypes.c_uint64]
+    L.moe_product_set_wait_limit.restype = _c_int
+    L.moe_block_scaled_product.argtypes = [_vp, _vp, _vp, _vp, _vp, _c_int, _vp, ctypes.c_int64,
+                                           _vp, ctypes.c_size_t, _vp]
+    L.moe_block_scaled_product.restype = _c_int
+    L.moe_product_device_status.argtypes = [_vp, _vp, _vp, ctypes.POINTER(ctypes.c_uint32)]
+    L.moe_product_device_status.restype = _c_int
     L.moe_pipeline_destroy.argtypes = [_vp]
     L.moe_pipeline_destroy.restype = None
     _lib = L
@@ -159,6 +190,7 @@ _I32 = ("int32",)
 _BF16 = ("bfloat16",)
 _MASK = ("uint8", "bool")
 _WEIGHT = ("bfloat16", "uint8", "float8_e4m3fn")
+_CODES = ("uint8", "float8_e4m3fn")
 
 
 def _addr(t, name: str = "argument", dtypes=None) -> int | None:
@@ -311,6 +343,106 @@ def moe_reduce_pairs(slab, k: int, n_extra: int, rows: int, H: int, w, valid, ou
                                  _addr(w, "w", _F32), _addr(valid, "valid", _MASK),
                                  _addr(out, "out", _BF16), _stream(stream))
     _check(st, "moe_reduce_pairs")
+
+
+def moe_forward_few(plan, weights: moe_weights, hidden, valid, T: int, k: int, out, workspace,
+                    ws_bytes: int, stream=None, dbg: moe_debug | None = None) -> None:
+    """moe_forward for T <= MOE_FEW_TOKENS_MAX tokens in one kernel."""
+    st = load().moe_forward_few(plan, ctypes.byref(weights), _addr(hidden, "hidden", _BF16),
+                                _addr(valid, "valid", _MASK), T, k, _addr(out, "out", _BF16),
+                                _addr(workspace, "workspace"), ws_bytes, _stream(stream),
+                                None if dbg is None else ctypes.byref(dbg))
+    _check(st, "moe_forward_few")
+
+
+def _on_one_device(**tensors):
+    """Every tensor on the current device: the library launches there."""
+    import torch
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda and t.device.index != cur:
+            raise ValueError(f"{name}: on {t.device}, the current device is cuda:{cur}")
+
+
+def _rows_of(t, name: str, dtypes) -> tuple[int, int]:
+    """(address, row stride in elements) of a 2-D CUDA tensor whose rows are contiguous;
+    the rows themselves may lie further apart, as in a slice of a wider tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is required, got one on {t.device}")
+    if str(t.dtype).rsplit(".", 1)[-1] not in dtypes:
+        raise ValueError(f"{name}: element type {t.dtype} is not one of {', '.join(dtypes)}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows of consecutive elements are required")
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name}: rows overlap (row stride {ld}, {cols} columns)")
+    return t.data_ptr(), ld
+
+
+def _groups(n: int) -> int:
+    return (n + 127) // 128
+
+
+def moe_quantize_groups(x, codes, scales, valid=None, gated: bool = False, stream=None) -> None:
+    """e4m3 codes [rows, cols] (uint8 or float8_e4m3fn) and fp32 scales [rows,
+    ceil(cols / 128)] of x [rows, cols] or, with ``gated``, of silu(g) * u for x = [g | u]
+    [rows, 2 cols].  x: bf16 or fp32, rows may be strided; valid: uint8 or bool [rows],
+    0 for padding rows, which get codes 0 and scales 1."""
+    if x.dim() != 2 or codes.dim() != 2:
+        raise ValueError("x and codes: two dimensions are required")
+    rows, cols = codes.shape
+    if tuple(x.shape) != (rows, cols * (2 if gated else 1)):
+        raise ValueError(f"x: shape {tuple(x.shape)} does not match codes {tuple(codes.shape)}"
+                         f"{' and gated' if gated else ''}")
+    if tuple(scales.shape) != (rows, _groups(cols)):
+        raise ValueError(f"scales: shape {tuple(scales.shape)}, needs {(rows, _groups(cols))}")
+    if valid is not None and tuple(valid.shape) != (rows,):
+        raise ValueError(f"valid: shape {tuple(valid.shape)}, needs ({rows},)")
+    addr, ld = _rows_of(x, "x", _BF16 + _F32)
+    c, s, v = (_addr(codes, "codes", _CODES), _addr(scales, "scales", _F32),
+               _addr(valid, "valid", _MASK))
+    _on_one_device(x=x, codes=codes, scales=scales, valid=valid)
+    _check(load().moe_quantize_groups(addr, MOE_T_FP32 if x.element_size() == 4 else MOE_T_BF16,
+                                      rows, cols, ld, int(bool(gated)), v, c, s, _stream(stream)),
+           "moe_quantize_groups")
+
+
+def moe_product_create(cfg: moe_product_config):
+    """Returns (product handle, workspace bytes)."""
+    h, n = _vp(), ctypes.c_size_t()
+    _check(load().moe_product_create(ctypes.byref(cfg), ctypes.byref(h), ctypes.byref(n)),
+           "moe_product_create")
+    return h.value, n.value
+
+
+def moe_product_destroy(product) -> None:
+    load().moe_product_destroy(product)
+
+
+def moe_product_set_wait_limit(product, limit_ns: int) -> None:
+    _check(load().moe_product_set_wait_limit(product, limit_ns), "moe_product_set_wait_limit")
+
+
+def moe_block_scaled_product(product, a, a_scales, w, w_scales, rows: int, out, ldo: int,
+                             workspace, ws_bytes: int, stream=None) -> None:
+    """out: a device address or tensor whose rows start ldo elements apart."""
+    st = load().moe_block_scaled_product(
+        product, _addr(a, "a", _CODES), _addr(a_scales, "a_scales", _F32), _addr(w, "w", _CODES),
+        _addr(w_scales, "w_scales", _F32), rows,
+        out if isinstance(out, int) else _rows_of(out, "out", _BF16 + _F32)[0], ldo,
+        _addr(workspace, "workspace"), ws_bytes, _stream(stream))
+    _check(st, "moe_block_scaled_product")
+
+
+def moe_product_device_status(product, workspace, stream=None) -> int:
+    """The device status bits of a product's workspace (0 = none); synchronises the stream."""
+    bits = ctypes.c_uint32()
+    st = load().moe_product_device_status(product, _addr(workspace, "workspace"), _stream(stream),
+                                          ctypes.byref(bits))
+    if st not in (MOE_OK, MOE_ERR_DEVICE):
+        raise MoeError(st, "moe_product_device_status")
+    return bits.value
 
 
 def moe_reduce_partials(slots, n_slots: int, rows: int, H: int, valid, out, stream=None) -> None:
@@ -496,6 +628,13 @@ class Plan:
         moe_forward(self.handle, weights, hidden, valid, self._rows(hidden, valid, out), k, out,
                     self.workspace, self.ws_bytes, stream, dbg)
 
+    def forward_few(self, weights: moe_weights, hidden, valid, k: int, out, stream=None, dbg=None):
+        """``forward`` for at most MOE_FEW_TOKENS_MAX tokens, in one kernel."""
+        T = self._rows(hidden, valid, out)
+        _on_one_device(hidden=hidden, valid=valid, out=out, workspace=self.workspace)
+        moe_forward_few(self.handle, weights, hidden, valid, T, k, out, self.workspace,
+                        self.ws_bytes, stream, dbg)
+
     def forward_scatter(self, weights: moe_weights, hidden, valid, k: int, dst,
                         rows_per_rank: int, slot: int, stream=None, dbg=None):
         T = self._rows(hidden, valid)
@@ -541,6 +680,58 @@ class Plan:
     def close(self):
         if self.handle:
             moe_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Product:
+    """A block-scaled product's shape plus a torch-allocated workspace on the current device."""
+
+    def __init__(self, *, max_rows: int, n: int, k: int, out_dtype=None, device=None):
+        import torch
+        types = {None: MOE_T_BF16, torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_FP32}
+        self.handle = None
+        if out_dtype not in types:
+            raise ValueError(f"out_dtype: {out_dtype} is neither bfloat16 nor float32")
+        self.cfg = moe_product_config(max_rows, n, k, types[out_dtype])
+        self.out_dtype = out_dtype or torch.bfloat16
+        self.handle, self.ws_bytes = moe_product_create(self.cfg)
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8,
+                                     device=device if device is not None else "cuda")
+
+    def forward(self, a, a_scales, w, w_scales, out, stream=None):
+        """out [rows, n] = (a scaled by a_scales) (w scaled by w_scales)^T: a e4m3 [rows, k],
+        a_scales fp32 [rows, ceil(k/128)], w e4m3 [n, k], w_scales fp32 [ceil(n/128),
+        ceil(k/128)].  Rows of out may be strided (a slice of a wider tensor)."""
+        n, k = self.cfg.n, self.cfg.k
+        rows = a.shape[0]
+        want = {"a": (a, (rows, k)), "a_scales": (a_scales, (rows, _groups(k))), "w": (w, (n, k)),
+                "w_scales": (w_scales, (_groups(n), _groups(k))), "out": (out, (rows, n))}
+        for name, (t, shape) in want.items():
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, the product needs {shape}")
+        if out.dtype != self.out_dtype:
+            raise ValueError(f"out: element type {out.dtype}, the product needs {self.out_dtype}")
+        ldo = _rows_of(out, "out", _BF16 + _F32)[1]
+        _on_one_device(a=a, a_scales=a_scales, w=w, w_scales=w_scales, out=out,
+                       workspace=self.workspace)
+        moe_block_scaled_product(self.handle, a, a_scales, w, w_scales, rows, out, ldo,
+                                 self.workspace, self.ws_bytes, stream)
+
+    def device_status(self, stream=None) -> int:
+        return moe_product_device_status(self.handle, self.workspace, stream)
+
+    def set_wait_limit(self, ns: int):
+        moe_product_set_wait_limit(self.handle, ns)
+
+    def close(self):
+        if self.handle:
+            moe_product_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

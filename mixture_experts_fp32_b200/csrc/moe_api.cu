@@ -4,9 +4,10 @@
 // device-to-host copy on the forward path.
 #include <string.h>
 
+#include <mutex>
 #include <new>
 
-#include "moe_internal.cuh"
+#include "weight_stream.cuh"
 
 #define MOE_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -20,6 +21,9 @@ struct moe_plan_s {
   size_t off_status, off_goff, off_done, off_wsplit, off_rscratch, off_partial, off_logits,
       off_ids, off_w, off_perm,
       off_inv, off_rowtok, off_xp, off_sx, off_h, off_sh, off_y;
+  // moe_forward_few
+  size_t off_few_logits, off_few_counters, off_few_part, off_few_hf;
+  int few_counters;
   unsigned long long wait_limit_ns;
   int device;
   int num_sms;
@@ -50,21 +54,9 @@ moe_status ensure_device(moe_plan_s* p) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   if (p->device == dev) return MOE_OK;
-  static unsigned long long prepared_mask = 0;   // devices whose kernel attributes are set
   int sms = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  int major = 0, minor = 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 0) return MOE_ERR_UNSUPPORTED;   // built for sm_100a only
-  if (dev < 64 && !((prepared_mask >> dev) & 1ull)) {
-    if (check_launch(moe::prepare_grouped_gemm_kernels()) != MOE_OK ||
-        check_launch(moe::prepare_grouped_gemm_fp8_kernels()) != MOE_OK ||
-        check_launch(moe::prepare_router_kernel()) != MOE_OK)
-      return MOE_ERR_CUDA;
-    prepared_mask |= 1ull << dev;
-  }
+  const moe_status s = moe::check_device(&sms, &dev);
+  if (s != MOE_OK) return s;
   p->num_sms = sms;
   p->device = dev;
   return MOE_OK;
@@ -88,6 +80,49 @@ moe_status check_common(const moe_plan_s* p, int T, int k, const void* workspace
 }
 
 }  // namespace
+
+namespace moe {
+
+moe_status cuda_status(cudaError_t e) { return check_launch(e); }
+
+moe_status check_device(int* num_sms, int* device) {
+  constexpr int kMaxDevices = 64;
+  static std::mutex mu;
+  static int sms_of[kMaxDevices];      // 0: not prepared yet
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return MOE_ERR_CUDA;
+  if (dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lock(mu);
+  if (sms_of[dev] == 0) {
+    int sms = 0, major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (major != 10 || minor != 0) return MOE_ERR_UNSUPPORTED;   // built for sm_100a only
+    if (check_launch(prepare_grouped_gemm_kernels()) != MOE_OK ||
+        check_launch(prepare_grouped_gemm_fp8_kernels()) != MOE_OK ||
+        check_launch(prepare_router_kernel()) != MOE_OK ||
+        check_launch(prepare_few_kernels()) != MOE_OK ||
+        check_launch(prepare_product_kernels()) != MOE_OK)
+      return MOE_ERR_CUDA;
+    sms_of[dev] = sms;
+  }
+  if (num_sms != nullptr) *num_sms = sms_of[dev];
+  if (device != nullptr) *device = dev;
+  return MOE_OK;
+}
+
+moe_status read_device_status(unsigned int* status, cudaStream_t st, uint32_t* bits) {
+  unsigned int v = 0;
+  if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaMemcpy(&v, status, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
+  if (v != 0 && cudaMemset(status, 0, sizeof(v)) != cudaSuccess) return MOE_ERR_CUDA;
+  if (bits != nullptr) *bits = v;
+  return v == 0 ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+}  // namespace moe
 
 MOE_EXPORT const char* moe_last_cuda_error_string(void) {
   return cudaGetErrorString(g_last_cuda_error);
@@ -167,6 +202,14 @@ MOE_EXPORT moe_status moe_plan_create(const moe_config* cfg, moe_plan_t* plan,
     p->off_sh = take(sizeof(float) * ((size_t)imax / 128) * r_cap);
     p->off_y = take(2 * r_cap * H);
   }
+  // moe_forward_few: router sums, counters, partial tiles, FP8: h before quantisation
+  const size_t few = T < MOE_FEW_TOKENS_MAX ? T : MOE_FEW_TOKENS_MAX;
+  p->few_counters = 3 * moe::kFewMaxCtas + (int)(few * ks) * (imax / 128);
+  p->off_few_logits =
+      take(sizeof(float) * moe::kFewRouterSplits * MOE_FEW_TOKENS_MAX * E);
+  p->off_few_counters = take(sizeof(unsigned int) * (size_t)p->few_counters);
+  p->off_few_part = take(sizeof(float) * moe::kFewMaxCtas * 4 * moe::kWsTileFloats);
+  p->off_few_hf = c.wtype == MOE_W_BF16 ? 0 : take(sizeof(float) * few * ks * (size_t)imax);
   p->ws_bytes = off;
   p->wait_limit_ns = 2000000000ull;
   p->device = -1;
@@ -203,20 +246,8 @@ MOE_EXPORT moe_status moe_split_router_weights(moe_plan_t plan, const float* rou
       plan->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
-// The forward pass; `co` says where the combine writes (the bf16 output, or
-// fp32 partial rows of a tensor- / expert-parallel rank), and [eb, ee) which
-// routed experts this call computes (their weights are the ones given).
-// Argument checks common to the entry points are here; each entry point checks
-// its own output arguments first.
-static moe_status forward_impl(moe_plan_t plan, const moe_weights* wts, const void* hidden,
-                               const uint8_t* valid, int T, int k, const moe::CombineOut& co,
-                               int eb, int ee, void* workspace, size_t ws_bytes, void* stream,
-                               moe_debug* dbg, const moe::SendArgs* send = nullptr) {
-  moe_status s = check_common(plan, T, k, workspace, ws_bytes);
-  if (s != MOE_OK) return s;
-  if (wts == nullptr) return MOE_ERR_INVALID_ARG;
-  if (T == 0) return MOE_OK;
-  const moe_config& c = plan->cfg;
+// The tensors of a forward: present and aligned as the kernels need them.
+static moe_status check_weights(const moe_config& c, const moe_weights* wts, const void* hidden) {
   const int S = c.num_shared;
   if (hidden == nullptr || wts->router_w == nullptr || wts->w_gate_up == nullptr ||
       wts->w_down == nullptr)
@@ -233,6 +264,25 @@ static moe_status forward_impl(moe_plan_t plan, const moe_weights* wts, const vo
       (wts->s_gate_up == nullptr || wts->s_down == nullptr ||
        (S && (wts->ss_gate_up == nullptr || wts->ss_down == nullptr))))
     return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// The forward pass; `co` says where the combine writes (the bf16 output, or
+// fp32 partial rows of a tensor- / expert-parallel rank), and [eb, ee) which
+// routed experts this call computes (their weights are the ones given).
+// Argument checks common to the entry points are here; each entry point checks
+// its own output arguments first.
+static moe_status forward_impl(moe_plan_t plan, const moe_weights* wts, const void* hidden,
+                               const uint8_t* valid, int T, int k, const moe::CombineOut& co,
+                               int eb, int ee, void* workspace, size_t ws_bytes, void* stream,
+                               moe_debug* dbg, const moe::SendArgs* send = nullptr) {
+  moe_status s = check_common(plan, T, k, workspace, ws_bytes);
+  if (s != MOE_OK) return s;
+  if (wts == nullptr) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  const moe_config& c = plan->cfg;
+  const int S = c.num_shared;
+  if ((s = check_weights(c, wts, hidden)) != MOE_OK) return s;
   s = ensure_device(plan);
   if (s != MOE_OK) return s;
   if (send != nullptr && (send->n_send < 1 || send->n_send >= plan->num_sms))
@@ -456,6 +506,75 @@ MOE_EXPORT moe_status moe_forward(moe_plan_t plan, const moe_weights* wts, const
                       ws_bytes, stream, dbg);
 }
 
+MOE_EXPORT moe_status moe_forward_few(moe_plan_t plan, const moe_weights* wts, const void* hidden,
+                                      const uint8_t* valid, int T, int k, void* out,
+                                      void* workspace, size_t ws_bytes, void* stream,
+                                      moe_debug* dbg) {
+  moe_status s = check_common(plan, T, k, workspace, ws_bytes);
+  if (s != MOE_OK) return s;
+  if (wts == nullptr) return MOE_ERR_INVALID_ARG;
+  if (T > MOE_FEW_TOKENS_MAX) return MOE_ERR_UNSUPPORTED;
+  if (dbg != nullptr && (dbg->perm != nullptr || dbg->offsets != nullptr))
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (out == nullptr || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  const moe_config& c = plan->cfg;
+  if ((s = check_weights(c, wts, hidden)) != MOE_OK) return s;
+  if ((s = ensure_device(plan)) != MOE_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool fp8 = c.wtype == MOE_W_FP8_E4M3_B128;
+  moe::FewArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = static_cast<const __nv_bfloat16*>(hidden);
+  a.valid = valid;
+  a.T = T;
+  a.H = c.hidden;
+  a.E = c.num_experts;
+  a.k = k;
+  a.S = c.num_shared;
+  a.I = c.inter;
+  a.Is = c.num_shared ? c.shared_inter : 0;
+  a.imax = plan->imax;
+  a.renorm = c.renormalize;
+  a.router_w = wts->router_w;
+  a.router_b = wts->router_b;
+  a.w_gate_up = static_cast<const uint8_t*>(wts->w_gate_up);
+  a.w_down = static_cast<const uint8_t*>(wts->w_down);
+  a.ws_gate_up = static_cast<const uint8_t*>(wts->ws_gate_up);
+  a.ws_down = static_cast<const uint8_t*>(wts->ws_down);
+  a.s_gate_up = wts->s_gate_up;
+  a.s_down = wts->s_down;
+  a.ss_gate_up = wts->ss_gate_up;
+  a.ss_down = wts->ss_down;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.logits = at<float>(workspace, plan->off_few_logits);
+  a.h = at<uint8_t>(workspace, plan->off_h);
+  a.h32 = at<float>(workspace, plan->off_few_hf);
+  a.sh = at<float>(workspace, plan->off_sh);
+  a.xq = at<uint8_t>(workspace, plan->off_xp);
+  a.sx = at<float>(workspace, plan->off_sx);
+  a.part = at<float>(workspace, plan->off_few_part);
+  a.counters = a.split_count = at<unsigned int>(workspace, plan->off_few_counters);
+  a.group_count = a.split_count + 3 * moe::kFewMaxCtas;
+  a.n_counters = plan->few_counters;
+  a.status = at<unsigned int>(workspace, plan->off_status);
+  a.bar = a.status + 16;               // beside the status word, cleared with it
+  a.timeout_bit = MOE_DEV_WAIT_TIMEOUT_FEW;
+  a.wait_limit_ns = plan->wait_limit_ns;
+  if (dbg != nullptr) {
+    a.logits_out = dbg->logits;
+    a.ids_out = dbg->topk_ids;
+    a.w_out = dbg->topk_w;
+  }
+  record(dbg, 0, st);
+  s = check_launch(cudaMemsetAsync(a.status, 0, kAlign, st));
+  if (s != MOE_OK) return s;
+  s = check_launch(moe::launch_few(a, fp8, plan->num_sms, st));
+  if (s != MOE_OK) return s;
+  record(dbg, MOE_NUM_STAGES, st);
+  return MOE_OK;
+}
+
 MOE_EXPORT moe_status moe_forward_scatter_experts(moe_plan_t plan, const moe_weights* wts,
                                                   const void* hidden, const uint8_t* valid, int T,
                                                   int k, float* const* dst, int n_dst,
@@ -581,14 +700,8 @@ MOE_EXPORT moe_status moe_route_from_logits(moe_plan_t plan, const float* logits
 MOE_EXPORT moe_status moe_check_device_status(moe_plan_t plan, void* workspace, void* stream,
                                               uint32_t* bits) {
   if (plan == nullptr || workspace == nullptr) return MOE_ERR_INVALID_ARG;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  unsigned int* status = at<unsigned int>(workspace, plan->off_status);
-  unsigned int v = 0;
-  if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
-  if (cudaMemcpy(&v, status, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-  if (v != 0 && cudaMemset(status, 0, sizeof(v)) != cudaSuccess) return MOE_ERR_CUDA;
-  if (bits != nullptr) *bits = v;
-  return v == 0 ? MOE_OK : MOE_ERR_DEVICE;
+  return moe::read_device_status(at<unsigned int>(workspace, plan->off_status),
+                                 static_cast<cudaStream_t>(stream), bits);
 }
 
 MOE_EXPORT moe_status moe_get_workspace_views(moe_plan_t plan, void* workspace,
@@ -654,7 +767,7 @@ void pipeline_release(moe_pipeline_s* q) {
   delete q;
 }
 
-moe_status cuda_status(cudaError_t e) { return check_launch(e); }
+using moe::cuda_status;
 
 // slot s's forward on the compute stream (the moe_forward launch sequence)
 moe_status pipeline_forward(moe_pipeline_s* q, int s) {

@@ -5,6 +5,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -155,6 +156,51 @@ cudaError_t launch_reduce_pairs(const float* slab, int k, int n_extra, int rows,
                                 const float* w, const uint8_t* valid, __nv_bfloat16* out,
                                 cudaStream_t st);
 cudaError_t prepare_grouped_gemm_kernels();
+
+// The few-token layer (few.cu).
+constexpr int kFewSlots = MOE_FEW_TOKENS_MAX * kMaxTopK;   // distinct experts, at most
+constexpr int kFewMaxCtas = 160;
+constexpr int kFewRouterSplits = 4;
+struct FewArgs {
+  const __nv_bfloat16* x;
+  const uint8_t* valid;
+  int T, H, E, k, S, I, Is, imax, renorm;
+  const float *router_w, *router_b;
+  const uint8_t *w_gate_up, *w_down, *ws_gate_up, *ws_down;    // bf16 or e4m3
+  const float *s_gate_up, *s_down, *ss_gate_up, *ss_down;
+  __nv_bfloat16* out;
+  // workspace
+  float* logits;                 // [router splits][MOE_FEW_TOKENS_MAX][E]
+  int router_splits, router_k;   // K splits of the router, values of K in each
+  uint8_t* h;                    // bf16: rows 2r (high part), 2r + 1 (low); FP8: codes of row r
+  float* h32;                    // FP8: h before quantisation [rows][imax]
+  float* sh;                     // FP8: scales of h
+  uint8_t* xq;                   // FP8: codes and scales of x
+  float* sx;
+  float* part;                   // partial tiles [CTA][2 ranges][head, tail]
+  unsigned int* counters;        // split_count and group_count together, zeroed by the kernel
+  int n_counters;
+  unsigned int* split_count;     // [3 ranges][kFewMaxCtas]
+  unsigned int* group_count;     // FP8: [S + selected experts][imax / 128]
+  unsigned int* bar;             // two grid barriers, zero before the launch
+  unsigned int* status;
+  unsigned int timeout_bit;
+  unsigned long long wait_limit_ns;
+  // optional copies
+  float* logits_out;
+  int* ids_out;
+  float* w_out;
+};
+cudaError_t launch_few(FewArgs a, bool fp8, int num_sms, cudaStream_t st);
+cudaError_t prepare_few_kernels();
+cudaError_t prepare_product_kernels();
+
+// Entry points' common parts (moe_api.cu).
+// The current device: sets the kernels' attributes on its first use, counts its SMs.
+moe_status check_device(int* num_sms = nullptr, int* device = nullptr);
+// MOE_OK, or MOE_ERR_CUDA with the error kept for moe_last_cuda_error_string.
+moe_status cuda_status(cudaError_t e);
+moe_status read_device_status(unsigned int* status, cudaStream_t st, uint32_t* bits);
 const moe_config* plan_config(const moe_plan_s* plan);
 void router_split_plan(int T, int E, int H, int num_sms, int partial_rows, int* splits,
                        int* kb_per_split);
@@ -165,6 +211,25 @@ void router_split_plan(int T, int E, int H, int num_sms, int partial_rows, int* 
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// Four e4m3 codes, saturating, ties to even.
+__device__ __forceinline__ uint32_t e4m3_codes4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// One 1x128 group by one warp, four values a lane: returns the lane's codes, sets the
+// group's scale (amax / 448; 1 if every value is zero).
+__device__ __forceinline__ uint32_t quantize_group_lane(const float (&v)[4], float* scale) {
+  float a = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+  const float s = a > 0.f ? __fdiv_rn(a, 448.f) : 1.f;
+  *scale = s;
+  return e4m3_codes4(__fdiv_rn(v[0], s), __fdiv_rn(v[1], s), __fdiv_rn(v[2], s),
+                     __fdiv_rn(v[3], s));
 }
 
 __device__ __forceinline__ uint64_t global_timer_ns() {

@@ -1,0 +1,205 @@
+// Streaming a weight matrix past a few activation rows: the pieces shared by the
+// few-token layer and the block-scaled product of few rows.
+//
+// Both read every weight once and multiply it with at most 8 * NT activation rows, so
+// they are bound by HBM, not by arithmetic: at 6.5 TB/s an SM receives about 23 bytes of
+// weights a clock, one m16n8k16 product every 22 clocks.  That decides the form:
+//  - weights travel by bulk copies into a ring of stages in shared memory (64 weight rows
+//    x 512 bytes of K each), which keeps 160 KB a CTA in flight whatever the consumers do,
+//    needs no tensor map (so nothing is encoded per call) and runs on across tiles,
+//    barriers and phases;
+//  - eight warps consume a stage, each a 64-byte slice of K of all 64 rows, as the A
+//    operand (weights on the M side, activation rows on the N side) of warp-wide
+//    m16n8k16 products.  The order of K inside a slice does not matter as long as both
+//    operands agree, so lane (g, q) takes 16 contiguous bytes of rows g and g + 8: one
+//    128-bit shared load per row feeds two (bf16) or four (e4m3) products, and the
+//    activation fragment is 16 contiguous bytes of its row, read straight from L2.
+//    tcgen05 would need 128-row tiles, accumulators in tensor memory and a round trip
+//    through it for every scale group, to save arithmetic that is not the bound;
+//  - the eight partial sums of a tile meet in shared memory once per tile.
+//
+// Work is cut into units of one stage.  Each CTA takes a contiguous range of the units
+// (within one unit of an even split, whatever the shapes); a tile whose units fall to
+// several CTAs is finished by the last of them to arrive, which adds the others'
+// partial tiles from global memory in CTA order, so results do not depend on timing.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+constexpr int kWsRows = 64;                   // weight rows of a stage
+constexpr int kWsBytes = 512;                 // bytes of K of a stage
+// rows 576 bytes apart: a quarter-warp's 128-bit loads (two rows, 64 bytes of each) then
+// fall on all 32 banks
+constexpr int kWsPitch = kWsBytes + 64;
+constexpr int kWsStageBytes = kWsRows * kWsPitch;
+constexpr int kWsWarps = 8;                   // consumers; warp w takes bytes 64w .. 64w + 63
+constexpr int kWsThreads = kWsWarps * 32;     // consumer threads
+constexpr int kWsBlock = kWsThreads + 32;     // and one producer warp
+// partial sums of a tile in shared memory: [warp][activation row][weight row], rows of 68
+// floats so that the fragments' stores are free of bank conflicts
+constexpr int kWsRedPitch = 68;
+constexpr int kWsTileFloats = 16 * kWsRows;   // a partial tile in global memory, 16 rows
+
+#if defined(__CUDACC__)
+
+// A CTA's share [begin, end) of `units`, and the CTA that owns a unit.
+__device__ __forceinline__ long long ws_begin(long long units, int cta, int ctas) {
+  return units * cta / ctas;
+}
+__device__ __forceinline__ int ws_owner(long long units, long long u, int ctas) {
+  return (int)(((u + 1) * ctas - 1) / units);
+}
+
+// Bounded wait taken by a whole warp (warp-uniform result): a limit of 0 gives up at once
+// unless the phase is already complete, any other suspends between looks.
+__device__ __forceinline__ bool ws_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns,
+                                        unsigned int* status, unsigned int bit) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, done)) return true;
+  if (limit_ns == 0) {
+    if ((threadIdx.x & 31) == 0) atomicOr(status, bit);
+    return false;
+  }
+  return mbar_wait_sleep_warp(bar, parity, limit_ns, status, bit);
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
+// Two e4m3 codes to two halves (exact: every e4m3 value is a half).
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
+  return r;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// One warp's slice of a stage: acc[m][n] += A(16 weight rows of m) * b[.][n]^T for the four
+// 16-row blocks m.  `slice`: shared address of this lane's 16 bytes in row g = lane / 4.
+// PARTS: activations given as a sum of PARTS terms (bf16 h as high and low part).
+// `live` false: this lane's 16 bytes lie past the end of K (left over from another stage)
+// and count as zero.
+template <bool FP8, int NT, int PARTS>
+__device__ __forceinline__ void ws_multiply(uint32_t slice, const uint4 (&b)[PARTS][NT], bool live,
+                                            float (&acc)[4][NT][4]) {
+  static_assert(!FP8 || PARTS == 1, "");
+  uint32_t bh[NT][8];
+  if (FP8) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t w[4] = {b[0][n].x, b[0][n].y, b[0][n].z, b[0][n].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bh[n][2 * i] = e4m3x2_to_half2(w[i] & 0xffffu);
+        bh[n][2 * i + 1] = e4m3x2_to_half2(w[i] >> 16);
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    uint4 lo = lds128(slice + (uint32_t)(m * 16 * kWsPitch));
+    uint4 hi = lds128(slice + (uint32_t)((m * 16 + 8) * kWsPitch));
+    if (!live) lo = hi = make_uint4(0, 0, 0, 0);
+    if (FP8) {
+      const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a0 = e4m3x2_to_half2(l[i] & 0xffffu), a2 = e4m3x2_to_half2(l[i] >> 16);
+        const uint32_t a1 = e4m3x2_to_half2(h[i] & 0xffffu), a3 = e4m3x2_to_half2(h[i] >> 16);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_f16(acc[m][n], a0, a1, a2, a3, bh[n][2 * i], bh[n][2 * i + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_bf16(acc[m][n], lo.x, hi.x, lo.y, hi.y, b[p][n].x, b[p][n].y);
+          mma_bf16(acc[m][n], lo.z, hi.z, lo.w, hi.w, b[p][n].z, b[p][n].w);
+        }
+    }
+  }
+}
+
+template <int NT>
+__device__ __forceinline__ void ws_zero(float (&a)[4][NT][4]) {
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[m][n][i] = 0.f;
+}
+
+// A warp's accumulators into its part of the shared partial sums.
+template <int NT>
+__device__ __forceinline__ void ws_park(float* red, int warp, int lane,
+                                        const float (&acc)[4][NT][4]) {
+  const int g = lane >> 2, q = lane & 3;
+  float* w = red + warp * (8 * NT * kWsRedPitch);
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[(n * 8 + 2 * q + (i & 1)) * kWsRedPitch + m * 16 + g + 8 * (i >> 1)] = acc[m][n][i];
+}
+
+// Sum over the warps, in warp order, of weight rows r, r + 1 of activation row t.
+template <int NT>
+__device__ __forceinline__ float2 ws_sum(const float* red, int t, int r) {
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kWsWarps; ++w) {
+    const float2 v =
+        *reinterpret_cast<const float2*>(red + (w * 8 * NT + t) * kWsRedPitch + r);
+    s.x += v.x;
+    s.y += v.y;
+  }
+  return s;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace moe
