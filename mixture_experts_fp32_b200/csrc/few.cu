@@ -24,18 +24,20 @@
 // first down rows while the CTAs meet after gate/up.  h keeps fp32's precision as two bf16
 // parts (bf16 weights), or is quantised per 1x128 group by the CTA that stores a group's
 // last tile (FP8).  Every sum is fp32 and in an order fixed by the shapes and the routing.
+#include <cudaTypedefs.h>
+
 #include "weight_stream.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kStages = 5;
 constexpr int kShared = kFewSlots;                    // slot of the shared expert
 constexpr unsigned long long kDrainNs = 1000000000ull;
 
 template <int NT>
 struct FewSmem {
-  alignas(16) uint8_t ring[kStages * kWsStageBytes];
+  static constexpr int kStages = NT == 1 ? 6 : 5;
+  alignas(1024) uint8_t ring[kStages * kWsStageBytes];
   alignas(16) float red[kWsWarps * 8 * NT * kWsRedPitch];
   float w[MOE_FEW_TOKENS_MAX][kMaxTopK];              // routing weights
   int ids[MOE_FEW_TOKENS_MAX][kMaxTopK];              // routed experts, -1 in padding rows
@@ -44,6 +46,10 @@ struct FewSmem {
   unsigned int bitmap[kMaxExperts / 32];
   uint64_t full[kStages], empty[kStages], routed;
   int flag;
+};
+
+struct FewMaps {
+  CUtensorMap gate_up, down, shared_gate_up, shared_down;
 };
 
 // (v, e) before (bv, be): larger logit first, then the lower expert index
@@ -59,9 +65,12 @@ __device__ __forceinline__ uint32_t two_bf16(float a, float b) {
 }
 
 template <bool FP8, int NT>
-__global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const FewArgs p) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  FewSmem<NT>& s = *reinterpret_cast<FewSmem<NT>*>(smem_raw);
+__global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant__ FewMaps maps,
+                                                          const FewArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  FewSmem<NT>& s = *reinterpret_cast<FewSmem<NT>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kStages = FewSmem<NT>::kStages;
   constexpr int TT = 8 * NT;                          // token columns
   constexpr int EB = FP8 ? 1 : 2;                     // bytes of a weight
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -91,33 +100,26 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const FewArgs p) {
     int stage = 0;
     uint32_t phase = 0, issued = 0, parity = 0;
     bool ok = true;
-    // lane i brings rows i and 32 + i of a unit
-    auto load = [&](const uint8_t* lo, const uint8_t* hi, size_t pitch, int koff, int bytes) {
+    auto load = [&](const CUtensorMap* m, int row0, int row1, int c, int row_bytes) {
       if (!ok) return;
-      ok = ws_wait(smem_u32(&s.empty[stage]), phase ^ 1u, p.wait_limit_ns, p.status,
-                                p.timeout_bit);
+      ok = ws_wait(smem_u32(&s.empty[stage]), phase ^ 1u, p.wait_limit_ns, p.status, p.timeout_bit);
       if (!ok) return;
-      const uint32_t bar = smem_u32(&s.full[stage]);
-      if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(kWsRows * bytes));
-      __syncwarp();
-      const uint32_t dst = smem_u32(s.ring + stage * kWsStageBytes) + lane * kWsPitch;
-      bulk_load(dst, lo + lane * pitch + koff, bytes, bar, once);
-      bulk_load(dst + 32 * kWsPitch, hi + lane * pitch + koff, bytes, bar, once);
+      ws_load_stage(smem_u32(s.ring + stage * kWsStageBytes), m, row0, row1, c * kWsBytes,
+                    min(kWsBytes, row_bytes - c * kWsBytes), smem_u32(&s.full[stage]), once);
       issued |= 1u << stage;
       parity = (parity & ~(1u << stage)) | (phase << stage);
       if (++stage == kStages) { stage = 0; phase ^= 1u; }
     };
-    auto gate_up = [&](const uint8_t* w, int I, long long u0, long long u1, bool routed) {
+    auto gate_up = [&](const CUtensorMap* m, int I, long long u0, long long u1, bool routed) {
       const int ft = I / 32;
       for (long long u = u0; u < u1 && ok; ++u) {
         const int tile = (int)(u / ch_h), c = (int)(u - (long long)tile * ch_h);
         const int slot = routed ? tile / ft : 0, f = (routed ? tile - slot * ft : tile) * 32;
-        const uint8_t* base = w + (routed ? (size_t)s.active[slot] * 2 * I * hb : 0);
-        load(base + (size_t)f * hb, base + (size_t)(I + f) * hb, hb, c * kWsBytes,
-             min(kWsBytes, hb - c * kWsBytes));
+        const int row = (routed ? s.active[slot] * 2 * I : 0) + f;
+        load(m, row, row + I, c, hb);
       }
     };
-    gate_up(p.ws_gate_up, p.Is, ws_begin(units_s, cta, ctas), ws_begin(units_s, cta + 1, ctas),
+    gate_up(&maps.shared_gate_up, p.Is, ws_begin(units_s, cta, ctas), ws_begin(units_s, cta + 1, ctas),
             false);
     if (ok)
       ok = ws_wait(smem_u32(&s.routed), 0, p.wait_limit_ns, p.status, p.timeout_bit);
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const FewArgs p) {
       int A = 0;
       for (int i = 0; i < kMaxExperts / 32; ++i) A += __popc(s.bitmap[i]);
       const long long units_r = (long long)A * (p.I / 32) * ch_h;
-      gate_up(p.w_gate_up, p.I, ws_begin(units_r, cta, ctas), ws_begin(units_r, cta + 1, ctas),
+      gate_up(&maps.gate_up, p.I, ws_begin(units_r, cta, ctas), ws_begin(units_r, cta + 1, ctas),
               true);
       if (A > 0) {
         const int per = ch_s + A * ch_i;              // stages of a down tile
@@ -134,24 +136,21 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const FewArgs p) {
         for (long long u = ws_begin(units, cta, ctas); u < u1 && ok; ++u) {
           const int tile = (int)(u / per);
           int c = (int)(u - (long long)tile * per);
-          const uint8_t* base = p.ws_down;
-          int rb = p.Is * EB;
-          if (c >= ch_s) {
+          const bool shared = c < ch_s;
+          int row = tile * 64;
+          if (!shared) {
             const int slot = (c - ch_s) / ch_i;
             c -= ch_s + slot * ch_i;
-            rb = p.I * EB;
-            base = p.w_down + (size_t)s.active[slot] * p.H * rb;
+            row += s.active[slot] * p.H;
           }
-          base += (size_t)tile * 64 * rb;
-          load(base, base + (size_t)32 * rb, rb, c * kWsBytes, min(kWsBytes, rb - c * kWsBytes));
+          load(shared ? &maps.shared_down : &maps.down, row, row + 32, c, (shared ? p.Is : p.I) * EB);
         }
       }
     }
     // no copy may still be writing when the CTA leaves
     for (int i = 0; i < kStages; ++i)
       if ((issued >> i) & 1u)
-        ws_wait(smem_u32(&s.full[i]), (parity >> i) & 1u, kDrainNs, p.status,
-                             p.timeout_bit);
+        ws_wait(smem_u32(&s.full[i]), (parity >> i) & 1u, kDrainNs, p.status, p.timeout_bit);
     return;
   }
 
@@ -335,11 +334,10 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const FewArgs p) {
   };
   int stage = 0;
   uint32_t phase = 0;
-  const uint32_t lane_off = (uint32_t)(g * kWsPitch + warp * 64 + q * 16);
+  const uint32_t lane_off = ws_lane_offset(warp, lane);
   auto stage_wait = [&]() {
     if (ok)
-      ok = ws_wait(smem_u32(&s.full[stage]), phase, p.wait_limit_ns, p.status,
-                                p.timeout_bit);
+      ok = ws_wait(smem_u32(&s.full[stage]), phase, p.wait_limit_ns, p.status, p.timeout_bit);
   };
   auto stage_done = [&]() {
     __syncwarp();
@@ -439,7 +437,7 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const FewArgs p) {
           if (FP8) {
             float part[4][NT][4];
             ws_zero<NT>(part);
-            ws_multiply<FP8, NT, 1>(slice, b, true, part);
+            ws_multiply<FP8, NT, 1>(slice, b, part);
 #pragma unroll
             for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -448,7 +446,7 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const FewArgs p) {
                 for (int i = 0; i < 4; ++i)
                   acc[m][n][i] = fmaf(part[m][n][i], (m < 2 ? fg : fu) * fa[n][i & 1], acc[m][n][i]);
           } else {
-            ws_multiply<FP8, NT, 1>(slice, b, true, acc);
+            ws_multiply<FP8, NT, 1>(slice, b, acc);
           }
         }
         stage_done();
@@ -602,8 +600,7 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const FewArgs p) {
       if (ok && __any_sync(0xffffffffu, keep != 0)) {
         float part[4][NT][4];
         ws_zero<NT>(part);
-        ws_multiply<FP8, NT, PARTS>(smem_u32(s.ring + stage * kWsStageBytes) + lane_off, b, true,
-                                    part);
+        ws_multiply<FP8, NT, PARTS>(smem_u32(s.ring + stage * kWsStageBytes) + lane_off, b, part);
         // a token that did not select this expert takes nothing from it, not even 0 * inf
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -652,28 +649,49 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const FewArgs p) {
 }
 
 template <bool FP8, int NT>
-cudaError_t launch(const FewArgs& a, int ctas, cudaStream_t st) {
+cudaError_t launch(const FewMaps& m, const FewArgs& a, int ctas, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(kWsBlock, 1, 1);
-  cfg.dynamicSmemBytes = sizeof(FewSmem<NT>);
+  cfg.dynamicSmemBytes = sizeof(FewSmem<NT>) + 1024;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];                        // the CTAs wait for one another
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_kernel<FP8, NT>, a);
+  return cudaLaunchKernelEx(&cfg, few_kernel<FP8, NT>, m, a);
 }
 
 template <bool FP8, int NT>
 cudaError_t prepare() {
-  static_assert(sizeof(FewSmem<NT>) <= 227 * 1024, "shared memory of one CTA");
+  static_assert(sizeof(FewSmem<NT>) + 1024 <= 227 * 1024, "shared memory of one CTA");
   return cudaFuncSetAttribute(few_kernel<FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)sizeof(FewSmem<NT>));
+                              (int)sizeof(FewSmem<NT>) + 1024);
 }
 
 }  // namespace
+
+bool ws_weight_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64_t rows) {
+  static const auto encode = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {row_bytes, rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {128, kWsBoxRows};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(w), dims, strides, box,
+                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t prepare_few_kernels() {
   cudaError_t e = prepare<false, 1>();
@@ -690,8 +708,20 @@ cudaError_t launch_few(FewArgs a, bool fp8, int num_sms, cudaStream_t st) {
   splits = splits < 1 ? 1 : splits > kFewRouterSplits ? kFewRouterSplits : splits;
   a.router_k = ((a.H + splits - 1) / splits + 255) / 256 * 256;
   a.router_splits = (a.H + a.router_k - 1) / a.router_k;
-  if (fp8) return a.T <= 8 ? launch<true, 1>(a, ctas, st) : launch<true, 2>(a, ctas, st);
-  return a.T <= 8 ? launch<false, 1>(a, ctas, st) : launch<false, 2>(a, ctas, st);
+  const uint64_t eb = fp8 ? 1 : 2, E = a.E, H = a.H, I = a.I, Is = a.Is;
+  FewMaps m;
+  if (!ws_weight_map(&m.gate_up, a.w_gate_up, H * eb, E * 2 * I) ||
+      !ws_weight_map(&m.down, a.w_down, I * eb, E * H))
+    return cudaErrorInvalidValue;
+  if (a.S == 0) {
+    m.shared_gate_up = m.gate_up;      // not used
+    m.shared_down = m.down;
+  } else if (!ws_weight_map(&m.shared_gate_up, a.ws_gate_up, H * eb, 2 * Is) ||
+             !ws_weight_map(&m.shared_down, a.ws_down, Is * eb, H)) {
+    return cudaErrorInvalidValue;
+  }
+  if (fp8) return a.T <= 8 ? launch<true, 1>(m, a, ctas, st) : launch<true, 2>(m, a, ctas, st);
+  return a.T <= 8 ? launch<false, 1>(m, a, ctas, st) : launch<false, 2>(m, a, ctas, st);
 }
 
 }  // namespace moe

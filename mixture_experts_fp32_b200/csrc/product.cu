@@ -21,7 +21,6 @@ struct moe_product_s {
 namespace moe {
 namespace {
 
-constexpr int kStages = 5;
 constexpr int kMaxCtas = 160;
 constexpr unsigned long long kDrainNs = 1000000000ull;
 
@@ -49,16 +48,20 @@ __device__ __forceinline__ void store_out(const ProductArgs& p, int m, int n, fl
 
 template <int NT>
 struct RowsSmem {
-  alignas(16) uint8_t ring[kStages * kWsStageBytes];
+  static constexpr int kStages = NT == 1 ? 6 : 5;
+  alignas(1024) uint8_t ring[kStages * kWsStageBytes];
   alignas(16) float red[kWsWarps * 8 * NT * kWsRedPitch];
   uint64_t full[kStages], empty[kStages];
   int flag;
 };
 
 template <int NT>
-__global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const ProductArgs p) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  RowsSmem<NT>& s = *reinterpret_cast<RowsSmem<NT>*>(smem_raw);
+__global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                                   const ProductArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  RowsSmem<NT>& s = *reinterpret_cast<RowsSmem<NT>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kStages = RowsSmem<NT>::kStages;
   constexpr int TT = 8 * NT;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
@@ -85,15 +88,9 @@ __global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const Product
       if (!ws_wait(smem_u32(&s.empty[stage]), phase ^ 1u, p.wait_limit_ns, p.status,
                                 kBit))
         break;
-      const int bytes = min(kWsBytes, p.K - c * kWsBytes);    // a multiple of 16
-      const int rows = min(kWsRows, p.N - tile * kWsRows);
-      const uint32_t bar = smem_u32(&s.full[stage]);
-      if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(rows * bytes));
-      __syncwarp();
-      const uint32_t dst = smem_u32(s.ring + stage * kWsStageBytes);
-      for (int r = lane; r < rows; r += 32)
-        bulk_load(dst + r * kWsPitch, p.w + (size_t)(tile * kWsRows + r) * p.K + c * kWsBytes,
-                  bytes, bar, once);
+      ws_load_stage(smem_u32(s.ring + stage * kWsStageBytes), &wmap, tile * kWsRows,
+                    tile * kWsRows + kWsBoxRows, c * kWsBytes, min(kWsBytes, p.K - c * kWsBytes),
+                    smem_u32(&s.full[stage]), once);
       issued |= 1u << stage;
       parity = (parity & ~(1u << stage)) | (phase << stage);
       if (++stage == kStages) { stage = 0; phase ^= 1u; }
@@ -109,7 +106,7 @@ __global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const Product
   bool ok = true;
   int stage = 0;
   uint32_t phase = 0;
-  const uint32_t lane_off = (uint32_t)(g * kWsPitch + warp * 64 + q * 16);
+  const uint32_t lane_off = ws_lane_offset(warp, lane);
   auto sync = []() { named_bar_sync(1, kWsThreads); };
   auto part_of = [&](int c, long long t0) {
     return p.part + (size_t)(c * 2 + (ws_begin(units, c, ctas) > t0 ? 0 : 1)) * kWsTileFloats;
@@ -120,10 +117,9 @@ __global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const Product
     const long long t0 = u - c0;
     u += c1 - c0;
     const float* sw = p.sw + (size_t)(tile * kWsRows / 128) * p.kb;
-    // the last 16 bytes of K may fall inside a warp's slice: lanes past them hold zero
-    auto fetch = [&](int c, uint4 (&b)[1][NT], float (&fa)[NT][2], bool& live) {
+    auto fetch = [&](int c, uint4 (&b)[1][NT], float (&fa)[NT][2]) {
       const int k = c * kWsBytes + warp * 64;
-      live = k + q * 16 < p.K;
+      const bool live = k + q * 16 < p.K;     // K may end inside the slice
       const float fw = k < p.K ? sw[k / 128] : 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -141,16 +137,15 @@ __global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const Product
     ws_zero<NT>(acc);
     uint4 b[1][NT], bn[1][NT];
     float fa[NT][2], fan[NT][2];
-    bool live, liven = false;
-    fetch(c0, b, fa, live);
+    fetch(c0, b, fa);
     for (int c = c0; c < c1; ++c) {
-      if (c + 1 < c1) fetch(c + 1, bn, fan, liven);
+      if (c + 1 < c1) fetch(c + 1, bn, fan);
       if (ok)
         ok = ws_wait(smem_u32(&s.full[stage]), phase, p.wait_limit_ns, p.status, kBit);
       if (ok && c * kWsBytes + warp * 64 < p.K) {
         float part[4][NT][4];
         ws_zero<NT>(part);
-        ws_multiply<true, NT, 1>(smem_u32(s.ring + stage * kWsStageBytes) + lane_off, b, live, part);
+        ws_multiply<true, NT, 1>(smem_u32(s.ring + stage * kWsStageBytes) + lane_off, b, part);
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -168,7 +163,6 @@ __global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const Product
         fa[n][0] = fan[n][0];
         fa[n][1] = fan[n][1];
       }
-      live = liven;
     }
     ws_park<NT>(s.red, warp, lane, acc);
     sync();
@@ -216,8 +210,8 @@ __global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const Product
 }
 
 template <int NT>
-cudaError_t launch_rows(const ProductArgs& a, int ctas, cudaStream_t st) {
-  product_rows_kernel<NT><<<ctas, kWsBlock, sizeof(RowsSmem<NT>), st>>>(a);
+cudaError_t launch_rows(const CUtensorMap& m, const ProductArgs& a, int ctas, cudaStream_t st) {
+  product_rows_kernel<NT><<<ctas, kWsBlock, sizeof(RowsSmem<NT>) + 1024, st>>>(m, a);
   return cudaGetLastError();
 }
 
@@ -226,10 +220,10 @@ cudaError_t launch_rows(const ProductArgs& a, int ctas, cudaStream_t st) {
 cudaError_t prepare_product_kernels() {
   cudaError_t e = cudaFuncSetAttribute(product_rows_kernel<1>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(RowsSmem<1>));
+                                       (int)sizeof(RowsSmem<1>) + 1024);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(product_rows_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sizeof(RowsSmem<2>));
+                             (int)sizeof(RowsSmem<2>) + 1024);
   return e;
 }
 
@@ -300,13 +294,15 @@ MOE_EXPORT moe_status moe_block_scaled_product(moe_product_t p, const void* a,
   g.status = reinterpret_cast<unsigned int*>(ws);
   g.wait_limit_ns = p->wait_limit_ns;
   const int ctas = sms < moe::kMaxCtas ? sms : moe::kMaxCtas;
+  CUtensorMap wmap;
+  if (!moe::ws_weight_map(&wmap, w, g.K, g.N)) return moe::cuda_status(cudaErrorInvalidValue);
   for (int m0 = 0; m0 < rows && s == MOE_OK; m0 += 16) {
     g.M = rows - m0 < 16 ? rows - m0 : 16;
     g.a = static_cast<const uint8_t*>(a) + (size_t)m0 * g.K;
     g.sa = a_scales + (size_t)m0 * g.kb;
     g.out = static_cast<uint8_t*>(out) + (size_t)m0 * ldo * (f32 ? 4 : 2);
-    s = moe::cuda_status(g.M <= 8 ? moe::launch_rows<1>(g, ctas, st)
-                                  : moe::launch_rows<2>(g, ctas, st));
+    s = moe::cuda_status(g.M <= 8 ? moe::launch_rows<1>(wmap, g, ctas, st)
+                                  : moe::launch_rows<2>(wmap, g, ctas, st));
   }
   return s;
 }

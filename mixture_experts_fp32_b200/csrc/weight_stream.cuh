@@ -4,10 +4,10 @@
 // Both read every weight once and multiply it with at most 8 * NT activation rows, so
 // they are bound by HBM, not by arithmetic: at 6.5 TB/s an SM receives about 23 bytes of
 // weights a clock, one m16n8k16 product every 22 clocks.  That decides the form:
-//  - weights travel by bulk copies into a ring of stages in shared memory (64 weight rows
-//    x 512 bytes of K each), which keeps 160 KB a CTA in flight whatever the consumers do,
-//    needs no tensor map (so nothing is encoded per call) and runs on across tiles,
-//    barriers and phases;
+//  - weights travel by TMA into a ring of stages in shared memory (64 weight rows x 512
+//    bytes of K each, eight boxes of 32 rows x 128 bytes), which keeps 160 KB or more a CTA
+//    in flight whatever the consumers do and runs on across tiles, barriers and phases.
+//    (Bulk copies of 512-byte row segments, which need no tensor map, brought 1.9 TB/s;)
 //  - eight warps consume a stage, each a 64-byte slice of K of all 64 rows, as the A
 //    operand (weights on the M side, activation rows on the N side) of warp-wide
 //    m16n8k16 products.  The order of K inside a slice does not matter as long as both
@@ -32,10 +32,10 @@ namespace moe {
 
 constexpr int kWsRows = 64;                   // weight rows of a stage
 constexpr int kWsBytes = 512;                 // bytes of K of a stage
-// rows 576 bytes apart: a quarter-warp's 128-bit loads (two rows, 64 bytes of each) then
-// fall on all 32 banks
-constexpr int kWsPitch = kWsBytes + 64;
-constexpr int kWsStageBytes = kWsRows * kWsPitch;
+constexpr int kWsBoxRows = 32;                // a box: 32 rows x 128 bytes, 128-byte swizzle
+constexpr int kWsBoxBytes = kWsBoxRows * 128;
+constexpr int kWsColumn = kWsRows * 128;      // 128 bytes of K of all 64 rows: two boxes
+constexpr int kWsStageBytes = kWsRows * kWsBytes;
 constexpr int kWsWarps = 8;                   // consumers; warp w takes bytes 64w .. 64w + 63
 constexpr int kWsThreads = kWsWarps * 32;     // consumer threads
 constexpr int kWsBlock = kWsThreads + 32;     // and one producer warp
@@ -43,6 +43,10 @@ constexpr int kWsBlock = kWsThreads + 32;     // and one producer warp
 // floats so that the fragments' stores are free of bank conflicts
 constexpr int kWsRedPitch = 68;
 constexpr int kWsTileFloats = 16 * kWsRows;   // a partial tile in global memory, 16 rows
+
+// Tensor map of a row-major weight matrix [rows, row_bytes] in boxes of 32 rows x 128 bytes;
+// what lies past its end reads as zero.
+bool ws_weight_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64_t rows);
 
 #if defined(__CUDACC__)
 
@@ -73,13 +77,29 @@ __device__ __forceinline__ bool ws_wait(uint32_t bar, uint32_t parity, unsigned 
   return mbar_wait_sleep_warp(bar, parity, limit_ns, status, bit);
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-      "[%0], [%1], %2, [%3], %4;" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
-      : "memory");
+// One stage by a warp: bytes [koff, koff + bytes) of K of weight rows row0 .. + 31 and
+// row1 .. + 31, a box a lane; `bytes` beyond a multiple of 128 arrive as zeros.
+__device__ __forceinline__ void ws_load_stage(uint32_t dst, const CUtensorMap* m, int row0,
+                                              int row1, int koff, int bytes, uint32_t bar,
+                                              uint64_t policy) {
+  const int lane = threadIdx.x & 31;
+  const int columns = (bytes + 127) / 128;
+  if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(columns * kWsColumn));
+  __syncwarp();
+  if (lane < 2 * columns)
+    tma_load_2d(dst + lane * kWsBoxBytes, m, koff + (lane >> 1) * 128, (lane & 1) ? row1 : row0,
+                bar, policy);
+}
+
+// Weight row (of a block of 8) that fragment row g holds: rows 4 apart for neighbouring g,
+// so that the 16-byte chunks of a quarter-warp, which the swizzle moves by the row's low
+// three bits, fall on all 32 banks.
+__device__ __forceinline__ int ws_row(int g) { return (g >> 1) | ((g & 1) << 2); }
+
+// Offset in a stage of a lane's 16 bytes of fragment row g = lane / 4 of the first block.
+__device__ __forceinline__ uint32_t ws_lane_offset(int warp, int lane) {
+  const int r = ws_row(lane >> 2), chunk = (warp & 1) * 4 + (lane & 3);
+  return (uint32_t)((warp >> 1) * kWsColumn + r * 128 + (chunk ^ r) * 16);
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -115,12 +135,10 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 }
 
 // One warp's slice of a stage: acc[m][n] += A(16 weight rows of m) * b[.][n]^T for the four
-// 16-row blocks m.  `slice`: shared address of this lane's 16 bytes in row g = lane / 4.
+// 16-row blocks m.  `slice`: shared address of this lane's 16 bytes in block row g = lane / 4.
 // PARTS: activations given as a sum of PARTS terms (bf16 h as high and low part).
-// `live` false: this lane's 16 bytes lie past the end of K (left over from another stage)
-// and count as zero.
 template <bool FP8, int NT, int PARTS>
-__device__ __forceinline__ void ws_multiply(uint32_t slice, const uint4 (&b)[PARTS][NT], bool live,
+__device__ __forceinline__ void ws_multiply(uint32_t slice, const uint4 (&b)[PARTS][NT],
                                             float (&acc)[4][NT][4]) {
   static_assert(!FP8 || PARTS == 1, "");
   uint32_t bh[NT][8];
@@ -137,9 +155,8 @@ __device__ __forceinline__ void ws_multiply(uint32_t slice, const uint4 (&b)[PAR
   }
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
-    uint4 lo = lds128(slice + (uint32_t)(m * 16 * kWsPitch));
-    uint4 hi = lds128(slice + (uint32_t)((m * 16 + 8) * kWsPitch));
-    if (!live) lo = hi = make_uint4(0, 0, 0, 0);
+    const uint4 lo = lds128(slice + (uint32_t)(m * 16 * 128));
+    const uint4 hi = lds128(slice + (uint32_t)((m * 16 + 8) * 128));
     if (FP8) {
       const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
@@ -175,7 +192,7 @@ __device__ __forceinline__ void ws_zero(float (&a)[4][NT][4]) {
 template <int NT>
 __device__ __forceinline__ void ws_park(float* red, int warp, int lane,
                                         const float (&acc)[4][NT][4]) {
-  const int g = lane >> 2, q = lane & 3;
+  const int r = ws_row(lane >> 2), q = lane & 3;
   float* w = red + warp * (8 * NT * kWsRedPitch);
 #pragma unroll
   for (int m = 0; m < 4; ++m)
@@ -183,7 +200,7 @@ __device__ __forceinline__ void ws_park(float* red, int warp, int lane,
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        w[(n * 8 + 2 * q + (i & 1)) * kWsRedPitch + m * 16 + g + 8 * (i >> 1)] = acc[m][n][i];
+        w[(n * 8 + 2 * q + (i & 1)) * kWsRedPitch + m * 16 + r + 8 * (i >> 1)] = acc[m][n][i];
 }
 
 // Sum over the warps, in warp order, of weight rows r, r + 1 of activation row t.
