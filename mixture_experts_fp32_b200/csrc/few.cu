@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
   const int ch_h = (hb + kWsBytes - 1) / kWsBytes;    // stages of a gate/up tile
   const int ch_i = (p.I * EB + kWsBytes - 1) / kWsBytes;
   const int ch_s = p.S ? (p.Is * EB + kWsBytes - 1) / kWsBytes : 0;
-  const long long units_s = p.S ? (long long)(p.Is / 32) * ch_h : 0;
+  const int units_s = p.S ? p.Is / 32 * ch_h : 0;
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -110,32 +110,31 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
       parity = (parity & ~(1u << stage)) | (phase << stage);
       if (++stage == kStages) { stage = 0; phase ^= 1u; }
     };
-    auto gate_up = [&](const CUtensorMap* m, int I, long long u0, long long u1, bool routed) {
+    auto gate_up = [&](const CUtensorMap* m, int I, int units, bool routed) {
       const int ft = I / 32;
-      for (long long u = u0; u < u1 && ok; ++u) {
-        const int tile = (int)(u / ch_h), c = (int)(u - (long long)tile * ch_h);
+      const WsSplit split(units, ctas);
+      const int u1 = split.begin(cta + 1);
+      for (int u = split.begin(cta); u < u1 && ok; ++u) {
+        const int tile = u / ch_h, c = u - tile * ch_h;
         const int slot = routed ? tile / ft : 0, f = (routed ? tile - slot * ft : tile) * 32;
         const int row = (routed ? s.active[slot] * 2 * I : 0) + f;
         load(m, row, row + I, c, hb);
       }
     };
-    gate_up(&maps.shared_gate_up, p.Is, ws_begin(units_s, cta, ctas), ws_begin(units_s, cta + 1, ctas),
-            false);
+    gate_up(&maps.shared_gate_up, p.Is, units_s, false);
     if (ok)
       ok = ws_wait(smem_u32(&s.routed), 0, p.wait_limit_ns, p.status, p.timeout_bit);
     if (ok) {
       int A = 0;
       for (int i = 0; i < kMaxExperts / 32; ++i) A += __popc(s.bitmap[i]);
-      const long long units_r = (long long)A * (p.I / 32) * ch_h;
-      gate_up(&maps.gate_up, p.I, ws_begin(units_r, cta, ctas), ws_begin(units_r, cta + 1, ctas),
-              true);
+      gate_up(&maps.gate_up, p.I, A * (p.I / 32) * ch_h, true);
       if (A > 0) {
         const int per = ch_s + A * ch_i;              // stages of a down tile
-        const long long units = (long long)(p.H / 64) * per;
-        const long long u1 = ws_begin(units, cta + 1, ctas);
-        for (long long u = ws_begin(units, cta, ctas); u < u1 && ok; ++u) {
-          const int tile = (int)(u / per);
-          int c = (int)(u - (long long)tile * per);
+        const WsSplit split(p.H / 64 * per, ctas);
+        const int u1 = split.begin(cta + 1);
+        for (int u = split.begin(cta); u < u1 && ok; ++u) {
+          const int tile = u / per;
+          int c = u - tile * per;
           const bool shared = c < ch_s;
           int row = tile * 64;
           if (!shared) {
@@ -189,19 +188,20 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[t] = 0.f;
     for (int k = k0 + warp * 256 + lane * 8; k < k1; k += kWsWarps * 256) {
-      const float4 w0 = *reinterpret_cast<const float4*>(wr + k);
-      const float4 w1 = *reinterpret_cast<const float4*>(wr + k + 4);
+      const float4 w0 = __ldg(reinterpret_cast<const float4*>(wr + k));
+      const float4 w1 = __ldg(reinterpret_cast<const float4*>(wr + k + 4));
+      const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+      uint4 xv[TT];                                   // columns past T repeat the last token
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+        xv[t] = __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)min(t, p.T - 1) * p.H + k));
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        if (t < p.T) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p.x + (size_t)t * p.H + k);
-          const uint32_t r[4] = {v.x, v.y, v.z, v.w};
-          const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        const uint32_t r[4] = {xv[t].x, xv[t].y, xv[t].z, xv[t].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            acc[t] = fmaf(__uint_as_float(r[i] << 16), w[2 * i], acc[t]);
-            acc[t] = fmaf(__uint_as_float(r[i] & 0xffff0000u), w[2 * i + 1], acc[t]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          acc[t] = fmaf(__uint_as_float(r[i] << 16), w[2 * i], acc[t]);
+          acc[t] = fmaf(__uint_as_float(r[i] & 0xffff0000u), w[2 * i + 1], acc[t]);
         }
       }
     }
@@ -240,17 +240,27 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
   // ---- 2a. the experts of every token, by every CTA for itself
   for (int t = warp; t < p.T; t += kWsWarps) {
     const bool real = p.valid == nullptr || p.valid[t];
-    float v[8];
+    float v[8], part[kFewRouterSplits][8], bias[8];
     uint32_t avail = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {                     // every load before the first use
+      const int e = lane + 32 * i;
+      bias[i] = e < p.E && p.router_b != nullptr ? p.router_b[e] : 0.f;
+#pragma unroll
+      for (int sp = 0; sp < kFewRouterSplits; ++sp)
+        part[sp][i] = e < p.E && sp < p.router_splits
+                          ? __ldcg(p.logits + ((size_t)sp * MOE_FEW_TOKENS_MAX + t) * p.E + e)
+                          : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = lane + 32 * i;
       v[i] = 0.f;
       if (e < p.E) {
         avail |= 1u << i;
-        for (int sp = 0; sp < p.router_splits; ++sp)
-          v[i] += __ldcg(p.logits + ((size_t)sp * MOE_FEW_TOKENS_MAX + t) * p.E + e);
-        if (p.router_b != nullptr) v[i] += p.router_b[e];
+#pragma unroll
+        for (int sp = 0; sp < kFewRouterSplits; ++sp) v[i] += part[sp][i];
+        v[i] += bias[i];
         if (cta == 0 && p.logits_out != nullptr)
           p.logits_out[(size_t)t * p.E + e] = real ? v[i] : 0.f;
       }
@@ -356,38 +366,14 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
     consumers_sync();
     return s.flag != 0;
   };
-  // partial tile of CTA c in range r (0: shared gate/up or down, 1: routed gate/up)
-  auto part_of = [&](int c, int r, long long units, long long t0) {
-    const bool head = ws_begin(units, c, ctas) > t0;
-    return p.part + (size_t)((c * 2 + r) * 2 + (head ? 0 : 1)) * kWsTileFloats;
-  };
-  // adds up rows r, r + 1 of activation row t over the CTAs that hold units of the tile
-  auto joined = [&](int range, long long units, long long t0, int per, int t, int r) {
-    float2 v = make_float2(0.f, 0.f);
-    const int b1 = ws_owner(units, t0 + per - 1, ctas);
-    for (int b = ws_owner(units, t0, ctas); b <= b1; ++b) {
-      if (ws_begin(units, b, ctas) == ws_begin(units, b + 1, ctas)) continue;
-      const float2 o = __ldcg(reinterpret_cast<const float2*>(
-          part_of(b, range, units, t0) + t * kWsRows + r));
-      v.x += o.x;
-      v.y += o.y;
-    }
-    return v;
-  };
-  auto sharers = [&](long long units, long long t0, int per) -> unsigned int {
-    if (units < ctas) return per;                     // one unit a CTA
-    return ws_owner(units, t0 + per - 1, ctas) - ws_owner(units, t0, ctas) + 1;
-  };
-
   // ---- 2b. gate/up
-  auto gate_up = [&](bool routed, int I, long long units, unsigned int* split_count) {
+  auto gate_up = [&](bool routed, int I, int units, unsigned int* split_count, float* parts) {
     const int ft = I / 32;
+    const WsSplit split(units, ctas);
     const uint8_t* xb = FP8 ? p.xq : reinterpret_cast<const uint8_t*>(p.x);
-    const long long u1 = ws_begin(units, cta + 1, ctas);
-    for (long long u = ws_begin(units, cta, ctas); u < u1;) {
-      const int tile = (int)(u / ch_h), c0 = (int)(u - (long long)tile * ch_h);
-      const int c1 = (int)min((long long)ch_h, c0 + (u1 - u));
-      const long long t0 = u - c0;
+    const int u1 = split.begin(cta + 1);
+    for (int u = split.begin(cta); u < u1;) {
+      const int tile = u / ch_h, c0 = u - tile * ch_h, c1 = min(ch_h, c0 + (u1 - u)), t0 = u - c0;
       u += c1 - c0;
       const int slot = routed ? tile / ft : kShared, f = (routed ? tile - slot * ft : tile) * 32;
       const int e = routed ? s.active[slot] : 0;
@@ -470,17 +456,17 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
         vu = ws_sum<NT>(s.red, t, 32 + r);
       }
       bool finish = true;
-      const int range = routed ? 1 : 0;
       if (c1 - c0 < ch_h) {
+        const int b0 = split.owner(t0), b1 = split.owner(t0 + ch_h - 1);
         if (mine) {
-          float* o = part_of(cta, range, units, t0) + t * kWsRows + r;
+          float* o = ws_partial(parts, cta, b0) + t * kWsRows + r;
           *reinterpret_cast<float2*>(o) = vg;
           *reinterpret_cast<float2*>(o + 32) = vu;
         }
-        finish = arrive_last(split_count + ws_owner(units, t0, ctas), sharers(units, t0, ch_h));
+        finish = arrive_last(split_count + b0, b1 - b0 + 1);
         if (finish && mine) {
-          vg = joined(range, units, t0, ch_h, t, r);
-          vu = joined(range, units, t0, ch_h, t, 32 + r);
+          vg = ws_joined(parts, b0, b1, t, r);
+          vu = ws_joined(parts, b0, b1, t, 32 + r);
         }
       }
       if (finish) {
@@ -520,11 +506,13 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
     }
   };
   if (A > 0) {
-    if (p.S) gate_up(false, p.Is, units_s, p.split_count);
-    gate_up(true, p.I, (long long)A * (p.I / 32) * ch_h, p.split_count + kFewMaxCtas);
+    if (p.S) gate_up(false, p.Is, units_s, p.split_count, p.part);
+    gate_up(true, p.I, A * (p.I / 32) * ch_h, p.split_count + kFewMaxCtas,
+            p.part + kFewMaxCtas * 2 * kWsTileFloats);
   } else {
     // every row is padding: nothing is computed, the shared rows that were loaded are let go
-    for (long long u = ws_begin(units_s, cta, ctas); u < ws_begin(units_s, cta + 1, ctas); ++u) {
+    const WsSplit split(units_s, ctas);
+    for (int u = split.begin(cta); u < split.begin(cta + 1); ++u) {
       stage_wait();
       stage_done();
     }
@@ -539,13 +527,11 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
     return;
   }
   const int per = ch_s + A * ch_i;
-  const long long units = (long long)(p.H / 64) * per;
-  const long long u1 = ws_begin(units, cta + 1, ctas);
+  const WsSplit down(p.H / 64 * per, ctas);
+  const int u1 = down.begin(cta + 1);
   constexpr int PARTS = FP8 ? 1 : 2;
-  for (long long u = ws_begin(units, cta, ctas); u < u1;) {
-    const int tile = (int)(u / per), c0 = (int)(u - (long long)tile * per);
-    const int c1 = (int)min((long long)per, c0 + (u1 - u));
-    const long long t0 = u - c0;
+  for (int u = down.begin(cta); u < u1;) {
+    const int tile = u / per, c0 = u - tile * per, c1 = min(per, c0 + (u1 - u)), t0 = u - c0;
     u += c1 - c0;
     // stage c of the tile: activation fragments and the factor of each token column
     auto fetch = [&](int c, uint4 (&b)[PARTS][NT], float (&fa)[NT][2], uint32_t& keep) {
@@ -626,20 +612,20 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
     consumers_sync();
     bool finish = true;
     const bool split = c1 - c0 < per;
+    const int b0 = down.owner(t0), b1 = down.owner(t0 + per - 1);
     if (split) {
       for (int i = tid; i < TT * 32; i += kWsThreads) {
         const int t = i >> 5, r = (i & 31) * 2;
-        *reinterpret_cast<float2*>(part_of(cta, 0, units, t0) + t * kWsRows + r) =
+        *reinterpret_cast<float2*>(ws_partial(p.part, cta, b0) + t * kWsRows + r) =
             ws_sum<NT>(s.red, t, r);
       }
-      finish = arrive_last(p.split_count + 2 * kFewMaxCtas + ws_owner(units, t0, ctas),
-                           sharers(units, t0, per));
+      finish = arrive_last(p.split_count + 2 * kFewMaxCtas + b0, b1 - b0 + 1);
     }
     if (finish) {
       for (int i = tid; i < TT * 32; i += kWsThreads) {
         const int t = i >> 5, r = (i & 31) * 2;
         if (t >= p.T) continue;
-        const float2 v = split ? joined(0, units, t0, per, t, r) : ws_sum<NT>(s.red, t, r);
+        const float2 v = split ? ws_joined(p.part, b0, b1, t, r) : ws_sum<NT>(s.red, t, r);
         *reinterpret_cast<uint32_t*>(p.out + (size_t)t * p.H + tile * 64 + r) =
             s.ids[t][0] >= 0 ? two_bf16(v.x, v.y) : 0u;
       }

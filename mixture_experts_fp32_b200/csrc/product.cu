@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const __grid_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
   const int per = (p.K + kWsBytes - 1) / kWsBytes;            // stages of a tile
-  const long long units = (long long)((p.N + kWsRows - 1) / kWsRows) * per;
-  const long long u1 = ws_begin(units, cta + 1, ctas);
+  const WsSplit split((p.N + kWsRows - 1) / kWsRows * per, ctas);
+  const int u1 = split.begin(cta + 1);
   constexpr unsigned int kBit = MOE_DEV_WAIT_TIMEOUT_PRODUCT;
 
   if (tid == 0) {
@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const __grid_
     const uint64_t once = policy_evict_first();
     int stage = 0;
     uint32_t phase = 0, issued = 0, parity = 0;
-    for (long long u = ws_begin(units, cta, ctas); u < u1; ++u) {
-      const int tile = (int)(u / per), c = (int)(u - (long long)tile * per);
+    for (int u = split.begin(cta); u < u1; ++u) {
+      const int tile = u / per, c = u - tile * per;
       if (!ws_wait(smem_u32(&s.empty[stage]), phase ^ 1u, p.wait_limit_ns, p.status,
                                 kBit))
         break;
@@ -108,13 +108,8 @@ __global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const __grid_
   uint32_t phase = 0;
   const uint32_t lane_off = ws_lane_offset(warp, lane);
   auto sync = []() { named_bar_sync(1, kWsThreads); };
-  auto part_of = [&](int c, long long t0) {
-    return p.part + (size_t)(c * 2 + (ws_begin(units, c, ctas) > t0 ? 0 : 1)) * kWsTileFloats;
-  };
-  for (long long u = ws_begin(units, cta, ctas); u < u1;) {
-    const int tile = (int)(u / per), c0 = (int)(u - (long long)tile * per);
-    const int c1 = (int)min((long long)per, c0 + (u1 - u));
-    const long long t0 = u - c0;
+  for (int u = split.begin(cta); u < u1;) {
+    const int tile = u / per, c0 = u - tile * per, c1 = min(per, c0 + (u1 - u)), t0 = u - c0;
     u += c1 - c0;
     const float* sw = p.sw + (size_t)(tile * kWsRows / 128) * p.kb;
     auto fetch = [&](int c, uint4 (&b)[1][NT], float (&fa)[NT][2]) {
@@ -167,18 +162,17 @@ __global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const __grid_
     ws_park<NT>(s.red, warp, lane, acc);
     sync();
     bool finish = true;
-    const bool split = c1 - c0 < per;
-    const int b0 = ws_owner(units, t0, ctas), b1 = ws_owner(units, t0 + per - 1, ctas);
-    if (split) {
+    const bool shared = c1 - c0 < per;
+    const int b0 = split.owner(t0), b1 = split.owner(t0 + per - 1);
+    if (shared) {
       for (int i = tid; i < TT * 32; i += kWsThreads) {
         const int t = i >> 5, r = (i & 31) * 2;
-        *reinterpret_cast<float2*>(part_of(cta, t0) + t * kWsRows + r) = ws_sum<NT>(s.red, t, r);
+        *reinterpret_cast<float2*>(ws_partial(p.part, cta, b0) + t * kWsRows + r) = ws_sum<NT>(s.red, t, r);
       }
       sync();
       if (tid == 0) {
         __threadfence();
-        const unsigned int n = units < ctas ? per : b1 - b0 + 1;
-        s.flag = atomicAdd(p.counters + b0, 1u) + 1 == n;
+        s.flag = atomicAdd(p.counters + b0, 1u) == (unsigned int)(b1 - b0);
         if (s.flag) p.counters[b0] = 0;               // as the next launch expects it
         __threadfence();
       }
@@ -189,18 +183,7 @@ __global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const __grid_
       for (int i = tid; i < TT * 32; i += kWsThreads) {
         const int t = i >> 5, r = (i & 31) * 2, n = tile * kWsRows + r;
         if (t >= p.M || n >= p.N) continue;
-        float2 v = make_float2(0.f, 0.f);
-        if (split) {
-          for (int c = b0; c <= b1; ++c) {
-            if (ws_begin(units, c, ctas) == ws_begin(units, c + 1, ctas)) continue;
-            const float2 o =
-                __ldcg(reinterpret_cast<const float2*>(part_of(c, t0) + t * kWsRows + r));
-            v.x += o.x;
-            v.y += o.y;
-          }
-        } else {
-          v = ws_sum<NT>(s.red, t, r);
-        }
+        const float2 v = shared ? ws_joined(p.part, b0, b1, t, r) : ws_sum<NT>(s.red, t, r);
         store_out(p, t, n, v.x);
         if (n + 1 < p.N) store_out(p, t, n + 1, v.y);
       }

@@ -50,12 +50,43 @@ bool ws_weight_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64_t r
 
 #if defined(__CUDACC__)
 
-// A CTA's share [begin, end) of `units`, and the CTA that owns a unit.
-__device__ __forceinline__ long long ws_begin(long long units, int cta, int ctas) {
-  return units * cta / ctas;
+// The even split of `units` over `ctas`: the first `more` CTAs take one unit more than `each`.
+// With fewer units than CTAs the CTAs behind the last unit have none.
+struct WsSplit {
+  int each, more;
+  __device__ __forceinline__ WsSplit(int units, int ctas)
+      : each(units / ctas), more(units - units / ctas * ctas) {}
+  __device__ __forceinline__ int begin(int cta) const { return cta * each + min(cta, more); }
+  __device__ __forceinline__ int owner(int u) const {
+    const int head = more * (each + 1);
+    return u < head ? u / (each + 1) : more + (u - head) / each;
+  }
+};
+
+// A tile that several CTAs share: CTA b's partial tile.  The first of them ends inside the
+// tile (its tail), the others begin inside it (their head); part: [CTA][head, tail].
+__device__ __forceinline__ float* ws_partial(float* part, int b, int first) {
+  return part + (size_t)(b * 2 + (b == first ? 1 : 0)) * kWsTileFloats;
 }
-__device__ __forceinline__ int ws_owner(long long units, long long u, int ctas) {
-  return (int)(((u + 1) * ctas - 1) / units);
+
+// Sum over CTAs b0 .. b1, in that order, of weight rows r, r + 1 of activation row t of their
+// partial tiles; the loads of eight CTAs go out together.
+__device__ __forceinline__ float2 ws_joined(float* part, int b0, int b1, int t, int r) {
+  float2 v = make_float2(0.f, 0.f);
+  for (int b = b0; b <= b1; b += 8) {
+    float2 o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      o[i] = b + i <= b1 ? __ldcg(reinterpret_cast<const float2*>(
+                               ws_partial(part, b + i, b0) + t * kWsRows + r))
+                         : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v.x += o[i].x;
+      v.y += o[i].y;
+    }
+  }
+  return v;
 }
 
 // Bounded wait taken by a whole warp (warp-uniform result): a limit of 0 gives up at once
