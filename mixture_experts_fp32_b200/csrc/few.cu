@@ -52,11 +52,6 @@ struct FewMaps {
   CUtensorMap gate_up, down, shared_gate_up, shared_down;
 };
 
-// (v, e) before (bv, be): larger logit first, then the lower expert index
-__device__ __forceinline__ bool before(float v, int e, float bv, int be) {
-  return v > bv || (v == bv && e < be);
-}
-
 __device__ __forceinline__ void consumers_sync() { named_bar_sync(1, kWsThreads); }
 
 __device__ __forceinline__ uint32_t two_bf16(float a, float b) {
@@ -240,89 +235,86 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
   // ---- 2a. the experts of every token, by every CTA for itself
   for (int t = warp; t < p.T; t += kWsWarps) {
     const bool real = p.valid == nullptr || p.valid[t];
-    float v[8], part[kFewRouterSplits][8], bias[8];
-    uint32_t avail = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {                     // every load before the first use
-      const int e = lane + 32 * i;
-      bias[i] = e < p.E && p.router_b != nullptr ? p.router_b[e] : 0.f;
-#pragma unroll
-      for (int sp = 0; sp < kFewRouterSplits; ++sp)
-        part[sp][i] = e < p.E && sp < p.router_splits
-                          ? __ldcg(p.logits + ((size_t)sp * MOE_FEW_TOKENS_MAX + t) * p.E + e)
-                          : 0.f;
-    }
+    // Logits as keys of their order (larger float, larger key; -0 as +0; at least 1, and 0 once
+    // taken), so that a round is two warp reductions: the largest key, then the lowest expert
+    // that has it.  The rounds are a loop, not unrolled: every launch fetches this code anew,
+    // and it runs once (unrolled, the selection took 11000 clocks for 8 experts, as a loop
+    // 3000).
+    float v[8];
+    uint32_t key[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = lane + 32 * i;
-      v[i] = 0.f;
+      float part[kFewRouterSplits], bias = 0.f;       // every load before the first use
       if (e < p.E) {
-        avail |= 1u << i;
+        if (p.router_b != nullptr) bias = p.router_b[e];
 #pragma unroll
-        for (int sp = 0; sp < kFewRouterSplits; ++sp) v[i] += part[sp][i];
-        v[i] += bias[i];
+        for (int sp = 0; sp < kFewRouterSplits; ++sp)
+          if (sp < p.router_splits)
+            part[sp] = __ldcg(p.logits + ((size_t)sp * MOE_FEW_TOKENS_MAX + t) * p.E + e);
+      }
+      v[i] = 0.f;
+      key[i] = 0;
+      if (e < p.E) {
+#pragma unroll
+        for (int sp = 0; sp < kFewRouterSplits; ++sp)
+          if (sp < p.router_splits) v[i] += part[sp];
+        v[i] += bias;
+        const uint32_t u = __float_as_uint(v[i] + 0.f);
+        key[i] = max(u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u), 1u);
         if (cta == 0 && p.logits_out != nullptr)
           p.logits_out[(size_t)t * p.E + e] = real ? v[i] : 0.f;
       }
     }
-    const uint32_t all = avail;
-    constexpr int kNone = 0x7fffffff;
-    int sel_e[kMaxTopK];
-    float sel_v[kMaxTopK];
+    int mine_e = -1;                                  // lane j: the j-th expert and its logit
+    float mine_v = 0.f;
+    if (real) {
+#pragma unroll 1
+      for (int j = 0; j < p.k; ++j) {
+        uint32_t best = 0;
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      sel_e[j] = 0;
-      sel_v[j] = 0.f;
-      if (j >= p.k) continue;
-      float bv = 0.f;
-      int be = kNone;
+        for (int i = 0; i < 8; ++i) best = max(best, key[i]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        int e = kMaxExperts;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = lane + 32 * i;
-        if (((avail >> i) & 1u) && (be == kNone || before(v[i], e, bv, be))) { bv = v[i]; be = e; }
+        for (int i = 7; i >= 0; --i)
+          if (key[i] == best) e = lane + 32 * i;
+        e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (e == lane + 32 * i) key[i] = 0;
+        if (lane == j) {
+          mine_e = e;
+          mine_v = __uint_as_float(best ^ ((best >> 31) ? 0x80000000u : 0xffffffffu));
+        }
       }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        const float ov = __shfl_xor_sync(0xffffffffu, bv, off);
-        const int oe = __shfl_xor_sync(0xffffffffu, be, off);
-        if (oe != kNone && (be == kNone || before(ov, oe, bv, be))) { bv = ov; be = oe; }
-      }
-      // every lane must hold the same choice, also where NaN logits make the order partial
-      be = __shfl_sync(0xffffffffu, be, 0);
-      bv = __shfl_sync(0xffffffffu, bv, 0);
-      sel_e[j] = be;
-      sel_v[j] = bv;
-      if ((be & 31) == lane) avail &= ~(1u << (be >> 5));
     }
-    float z = 0.f;
-    if (p.renorm) {
-#pragma unroll
-      for (int j = 0; j < kMaxTopK; ++j)
-        if (j < p.k) z += expf(sel_v[j] - sel_v[0]);
-    } else {
+    const float top = __shfl_sync(0xffffffffu, mine_v, 0);
+    const float ex = real && lane < p.k ? expf(mine_v - top) : 0.f;
+    float z = ex;
+    if (!p.renorm) {
+      z = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if ((all >> i) & 1u) z += expf(v[i] - sel_v[0]);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+        if (lane + 32 * i < p.E) z += expf(v[i] - top);
     }
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      if (j < p.k && lane == j) {
-        const int e = real ? sel_e[j] : -1;
-        const float w = real ? expf(sel_v[j] - sel_v[0]) / z : 0.f;
-        s.ids[t][j] = e;
-        s.w[t][j] = w;
-        if (real) atomicOr(&s.bitmap[e >> 5], 1u << (e & 31));
-        if (cta == 0 && p.ids_out != nullptr) p.ids_out[t * p.k + j] = e;
-        if (cta == 0 && p.w_out != nullptr) p.w_out[t * p.k + j] = w;
-      }
+    for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+    if (lane < p.k) {
+      const float w = real ? ex / z : 0.f;
+      s.ids[t][lane] = mine_e;
+      s.w[t][lane] = w;
+      if (real) atomicOr(&s.bitmap[mine_e >> 5], 1u << (mine_e & 31));
+      if (cta == 0 && p.ids_out != nullptr) p.ids_out[t * p.k + lane] = mine_e;
+      if (cta == 0 && p.w_out != nullptr) p.w_out[t * p.k + lane] = w;
     }
   }
   consumers_sync();
   auto rank_of = [&](int e) {
     int r = __popc(s.bitmap[e >> 5] & ((1u << (e & 31)) - 1u));
-    for (int i = 0; i < (e >> 5); ++i) r += __popc(s.bitmap[i]);
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32 - 1; ++i)
+      if (i < (e >> 5)) r += __popc(s.bitmap[i]);
     return r;
   };
   if (tid < p.E && ((s.bitmap[tid >> 5] >> (tid & 31)) & 1u)) s.active[rank_of(tid)] = (short)tid;
@@ -384,66 +376,71 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
         sw_gate = sw + (size_t)(f / 128) * kb_h;
         sw_up = sw + (size_t)((I + f) / 128) * kb_h;
       }
-      bool on[NT];
+      bool on[NT], on2[NT][2];                        // tokens of this lane's fragment, columns
 #pragma unroll
-      for (int n = 0; n < NT; ++n) on[n] = h_row(slot, n * 8 + g) >= 0;
-      auto fetch = [&](int c, uint4 (&b)[1][NT], float (&fa)[NT][2], float& fg, float& fu) {
+      for (int n = 0; n < NT; ++n) {
+        on[n] = h_row(slot, n * 8 + g) >= 0;
+        on2[n][0] = h_row(slot, n * 8 + 2 * q) >= 0;
+        on2[n][1] = h_row(slot, n * 8 + 2 * q + 1) >= 0;
+      }
+      struct Frag {
+        uint4 b[1][NT];
+        float fa[NT][2], fg, fu;                      // FP8: scales of tokens, gate and up rows
+      };
+      auto fetch = [&](int c, Frag& x) {
         const int kbyte = c * kWsBytes + warp * 64;
         const bool live = kbyte < hb;                 // H is a multiple of 128: all or nothing
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          b[0][n] = make_uint4(0, 0, 0, 0);
+          x.b[0][n] = make_uint4(0, 0, 0, 0);
           if (live && on[n])
-            b[0][n] = __ldcg(reinterpret_cast<const uint4*>(xb + (size_t)(n * 8 + g) * hb + kbyte +
-                                                            q * 16));
+            x.b[0][n] = __ldcg(reinterpret_cast<const uint4*>(xb + (size_t)(n * 8 + g) * hb +
+                                                              kbyte + q * 16));
           if (FP8) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int t = n * 8 + 2 * q + i;
-              fa[n][i] = live && h_row(slot, t) >= 0 ? __ldcg(p.sx + (size_t)t * kb_h + kbyte / 128)
-                                                     : 0.f;
-            }
+            for (int i = 0; i < 2; ++i)
+              x.fa[n][i] = live && on2[n][i]
+                               ? __ldcg(p.sx + (size_t)(n * 8 + 2 * q + i) * kb_h + kbyte / 128)
+                               : 0.f;
           }
         }
         if (FP8) {
-          fg = live ? sw_gate[kbyte / 128] : 0.f;
-          fu = live ? sw_up[kbyte / 128] : 0.f;
+          x.fg = live ? sw_gate[kbyte / 128] : 0.f;
+          x.fu = live ? sw_up[kbyte / 128] : 0.f;
         }
       };
       float acc[4][NT][4];
       ws_zero<NT>(acc);
-      uint4 b[1][NT], bn[1][NT];
-      float fa[NT][2], fan[NT][2], fg = 1.f, fu = 1.f, fgn = 1.f, fun = 1.f;
-      fetch(c0, b, fa, fg, fu);
-      for (int c = c0; c < c1; ++c) {
-        if (c + 1 < c1) fetch(c + 1, bn, fan, fgn, fun);
-        stage_wait();
-        if (ok && c * kWsBytes + warp * 64 < hb) {
-          const uint32_t slice = smem_u32(s.ring + stage * kWsStageBytes) + lane_off;
-          if (FP8) {
-            float part[4][NT][4];
-            ws_zero<NT>(part);
-            ws_multiply<FP8, NT, 1>(slice, b, part);
+      // fragments of two stages are under way while a third is multiplied
+      Frag x[3];
+      fetch(c0, x[0]);
+      if (c0 + 1 < c1) fetch(c0 + 1, x[1]);
+      for (int c = c0; c < c1; c += 3) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+        for (int j = 0; j < 3; ++j) {
+          if (c + j >= c1) break;
+          if (c + j + 2 < c1) fetch(c + j + 2, x[(j + 2) % 3]);
+          stage_wait();
+          if (ok && (c + j) * kWsBytes + warp * 64 < hb) {
+            const uint32_t slice = smem_u32(s.ring + stage * kWsStageBytes) + lane_off;
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
+            for (int m = 0; m < 4; ++m) {
+              if (FP8) {
+                float part[NT][4] = {};
+                ws_multiply<FP8, NT, 1>(slice, m, x[j].b, part);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  acc[m][n][i] = fmaf(part[m][n][i], (m < 2 ? fg : fu) * fa[n][i & 1], acc[m][n][i]);
-          } else {
-            ws_multiply<FP8, NT, 1>(slice, b, acc);
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    acc[m][n][i] = fmaf(part[n][i], (m < 2 ? x[j].fg : x[j].fu) * x[j].fa[n][i & 1],
+                                        acc[m][n][i]);
+              } else {
+                ws_multiply<FP8, NT, 1>(slice, m, x[j].b, acc[m]);
+              }
+            }
           }
+          stage_done();
         }
-        stage_done();
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          b[0][n] = bn[0][n];
-          fa[n][0] = fan[n][0];
-          fa[n][1] = fan[n][1];
-        }
-        fg = fgn;
-        fu = fun;
       }
       ws_park<NT>(s.red, warp, lane, acc);
       consumers_sync();
@@ -533,8 +530,14 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
   for (int u = down.begin(cta); u < u1;) {
     const int tile = u / per, c0 = u - tile * per, c1 = min(per, c0 + (u1 - u)), t0 = u - c0;
     u += c1 - c0;
-    // stage c of the tile: activation fragments and the factor of each token column
-    auto fetch = [&](int c, uint4 (&b)[PARTS][NT], float (&fa)[NT][2], uint32_t& keep) {
+    // stage c of the tile: activation fragments, the factor of each token column, and which
+    // of the columns take part
+    struct Frag {
+      uint4 b[PARTS][NT];
+      float fh[NT][2], fw;                            // FP8: scales of h and of the weights
+      int slot;                                       // -1: past the segment's K
+    };
+    auto fetch = [&](int c, Frag& x) {
       int slot = kShared, ci = c, width = p.Is;
       if (c >= ch_s) {
         slot = (c - ch_s) / ch_i;
@@ -543,70 +546,73 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
       }
       const int kbyte = ci * kWsBytes + warp * 64;
       const bool live = kbyte < width * EB;
-      float fw = 1.f;
+      x.slot = live ? slot : -1;
+      x.fw = 1.f;
       if (FP8 && live) {
         const int rb = tile * 64 / 128, kbs = width / 128;
-        fw = slot == kShared
+        x.fw = slot == kShared
                  ? p.ss_down[(size_t)rb * kbs + kbyte / 128]
                  : p.s_down[((size_t)s.active[slot] * kb_h + rb) * kbs + kbyte / 128];
       }
-      keep = 0;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int row = live ? h_row(slot, n * 8 + g) : -1;
 #pragma unroll
         for (int w = 0; w < PARTS; ++w) {
-          b[w][n] = make_uint4(0, 0, 0, 0);
+          x.b[w][n] = make_uint4(0, 0, 0, 0);
           if (row >= 0)
-            b[w][n] = __ldcg(reinterpret_cast<const uint4*>(
+            x.b[w][n] = __ldcg(reinterpret_cast<const uint4*>(
                 p.h + ((size_t)row * PARTS + w) * p.imax * EB + kbyte + q * 16));
         }
+        if (FP8) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = n * 8 + 2 * q + i, hr = live ? h_row(slot, t) : -1;
-          fa[n][i] = 0.f;
-          if (hr >= 0) {
-            keep |= 1u << (2 * n + i);
-            float v = slot == kShared ? 1.f : s.w[t][(int)s.pick[slot][t]];
-            if (FP8) v *= fw * __ldcg(p.sh + (size_t)hr * kb_i + kbyte / 128);
-            fa[n][i] = v;
+          for (int i = 0; i < 2; ++i) {
+            const int hr = live ? h_row(slot, n * 8 + 2 * q + i) : -1;
+            x.fh[n][i] = hr >= 0 ? __ldcg(p.sh + (size_t)hr * kb_i + kbyte / 128) : 0.f;
           }
         }
       }
     };
     float acc[4][NT][4];
     ws_zero<NT>(acc);
-    uint4 b[PARTS][NT], bn[PARTS][NT];
-    float fa[NT][2], fan[NT][2];
-    uint32_t keep = 0, keepn = 0;
-    fetch(c0, b, fa, keep);
-    for (int c = c0; c < c1; ++c) {
-      if (c + 1 < c1) fetch(c + 1, bn, fan, keepn);
-      stage_wait();
-      if (ok && __any_sync(0xffffffffu, keep != 0)) {
-        float part[4][NT][4];
-        ws_zero<NT>(part);
-        ws_multiply<FP8, NT, PARTS>(smem_u32(s.ring + stage * kWsStageBytes) + lane_off, b, part);
-        // a token that did not select this expert takes nothing from it, not even 0 * inf
+    Frag x[3];
+    fetch(c0, x[0]);
+    if (c0 + 1 < c1) fetch(c0 + 1, x[1]);
+    for (int c = c0; c < c1; c += 3) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int j = 0; j < 3; ++j) {
+        if (c + j >= c1) break;
+        if (c + j + 2 < c1) fetch(c + j + 2, x[(j + 2) % 3]);
+        stage_wait();
+        if (ok && x[j].slot >= 0) {
+          // the factor of each token column, and which columns take part
+          float f[NT][2];
+          uint32_t keep = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if ((keep >> (2 * n + (i & 1))) & 1u) {
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int m = 0; m < 4; ++m)
-                acc[m][n][i] = fmaf(part[m][n][i], fa[n][i & 1], acc[m][n][i]);
+            for (int i = 0; i < 2; ++i) {
+              const int t = n * 8 + 2 * q + i, pick = s.pick[x[j].slot][t];
+              if (pick >= 0) keep |= 1u << (2 * n + i);
+              f[n][i] = x[j].slot == kShared || pick < 0 ? 1.f : s.w[t][pick];
+              if (FP8) f[n][i] *= x[j].fw * x[j].fh[n][i];
             }
-      }
-      stage_done();
+          const uint32_t slice = smem_u32(s.ring + stage * kWsStageBytes) + lane_off;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+          for (int m = 0; m < 4; ++m) {
+            float part[NT][4] = {};
+            ws_multiply<FP8, NT, PARTS>(slice, m, x[j].b, part);
+            // a token that did not select this expert takes nothing from it, not even 0 * inf
 #pragma unroll
-        for (int w = 0; w < PARTS; ++w) b[w][n] = bn[w][n];
-        fa[n][0] = fan[n][0];
-        fa[n][1] = fan[n][1];
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if ((keep >> (2 * n + (i & 1))) & 1u)
+                  acc[m][n][i] = fmaf(part[n][i], f[n][i & 1], acc[m][n][i]);
+          }
+        }
+        stage_done();
       }
-      keep = keepn;
     }
     ws_park<NT>(s.red, warp, lane, acc);
     consumers_sync();

@@ -112,51 +112,55 @@ __global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const __grid_
     const int tile = u / per, c0 = u - tile * per, c1 = min(per, c0 + (u1 - u)), t0 = u - c0;
     u += c1 - c0;
     const float* sw = p.sw + (size_t)(tile * kWsRows / 128) * p.kb;
-    auto fetch = [&](int c, uint4 (&b)[1][NT], float (&fa)[NT][2]) {
+    struct Frag {
+      uint4 b[1][NT];
+      float fa[NT][2], fw;                    // multiplied where they are used: loads stay ahead
+    };
+    auto fetch = [&](int c, Frag& x) {
       const int k = c * kWsBytes + warp * 64;
       const bool live = k + q * 16 < p.K;     // K may end inside the slice
-      const float fw = k < p.K ? sw[k / 128] : 0.f;
+      x.fw = k < p.K ? __ldg(sw + k / 128) : 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        b[0][n] = make_uint4(0, 0, 0, 0);
+        x.b[0][n] = make_uint4(0, 0, 0, 0);
         if (live && n * 8 + g < p.M)
-          b[0][n] = __ldg(reinterpret_cast<const uint4*>(p.a + (size_t)(n * 8 + g) * p.K + k + q * 16));
+          x.b[0][n] =
+              __ldg(reinterpret_cast<const uint4*>(p.a + (size_t)(n * 8 + g) * p.K + k + q * 16));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t = n * 8 + 2 * q + i;
-          fa[n][i] = k < p.K && t < p.M ? fw * __ldg(p.sa + (size_t)t * p.kb + k / 128) : 0.f;
+          x.fa[n][i] = k < p.K && t < p.M ? __ldg(p.sa + (size_t)t * p.kb + k / 128) : 0.f;
         }
       }
     };
     float acc[4][NT][4];
     ws_zero<NT>(acc);
-    uint4 b[1][NT], bn[1][NT];
-    float fa[NT][2], fan[NT][2];
-    fetch(c0, b, fa);
-    for (int c = c0; c < c1; ++c) {
-      if (c + 1 < c1) fetch(c + 1, bn, fan);
-      if (ok)
-        ok = ws_wait(smem_u32(&s.full[stage]), phase, p.wait_limit_ns, p.status, kBit);
-      if (ok && c * kWsBytes + warp * 64 < p.K) {
-        float part[4][NT][4];
-        ws_zero<NT>(part);
-        ws_multiply<true, NT, 1>(smem_u32(s.ring + stage * kWsStageBytes) + lane_off, b, part);
+    // fragments of two stages are under way while a third is multiplied
+    Frag x[3];
+    fetch(c0, x[0]);
+    if (c0 + 1 < c1) fetch(c0 + 1, x[1]);
+    for (int c = c0; c < c1; c += 3) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+      for (int j = 0; j < 3; ++j) {
+        if (c + j >= c1) break;
+        if (c + j + 2 < c1) fetch(c + j + 2, x[(j + 2) % 3]);
+        if (ok) ok = ws_wait(smem_u32(&s.full[stage]), phase, p.wait_limit_ns, p.status, kBit);
+        if (ok && (c + j) * kWsBytes + warp * 64 < p.K) {
+          const uint32_t slice = smem_u32(s.ring + stage * kWsStageBytes) + lane_off;
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int m = 0; m < 4; ++m) {
+            float part[NT][4] = {};
+            ws_multiply<true, NT, 1>(slice, m, x[j].b, part);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[m][n][i] = fmaf(part[m][n][i], fa[n][i & 1], acc[m][n][i]);
-      }
-      __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(smem_u32(&s.empty[stage]));
-      if (++stage == kStages) { stage = 0; phase ^= 1u; }
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        b[0][n] = bn[0][n];
-        fa[n][0] = fan[n][0];
-        fa[n][1] = fan[n][1];
+              for (int i = 0; i < 4; ++i)
+                acc[m][n][i] = fmaf(part[n][i], x[j].fw * x[j].fa[n][i & 1], acc[m][n][i]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(smem_u32(&s.empty[stage]));
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
     }
     ws_park<NT>(s.red, warp, lane, acc);

@@ -9,10 +9,10 @@
 //    in flight whatever the consumers do and runs on across tiles, barriers and phases.
 //    (Bulk copies of 512-byte row segments, which need no tensor map, brought 1.9 TB/s;)
 //  - eight warps consume a stage, each a 64-byte slice of K of all 64 rows, as the A
-//    operand (weights on the M side, activation rows on the N side) of warp-wide
-//    m16n8k16 products.  The order of K inside a slice does not matter as long as both
+//    operand (weights on the M side, activation rows on the N side) of warp-wide m16n8
+//    products (k16 bf16, k32 e4m3).  The order of K inside a slice does not matter as long as both
 //    operands agree, so lane (g, q) takes 16 contiguous bytes of rows g and g + 8: one
-//    128-bit shared load per row feeds two (bf16) or four (e4m3) products, and the
+//    128-bit shared load per row feeds two products, and the
 //    activation fragment is 16 contiguous bytes of its row, read straight from L2.
 //    tcgen05 would need 128-row tiles, accumulators in tensor memory and a round trip
 //    through it for every scale group, to save arithmetic that is not the bound;
@@ -23,8 +23,6 @@
 // several CTAs is finished by the last of them to arrive, which adds the others'
 // partial tiles from global memory in CTA order, so results do not depend on timing.
 #pragma once
-
-#include <cuda_fp16.h>
 
 #include "moe_internal.cuh"
 
@@ -141,13 +139,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
-// Two e4m3 codes to two halves (exact: every e4m3 value is a half).
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
-  return r;
-}
-
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -156,57 +147,35 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One warp's slice of a stage: acc[m][n] += A(16 weight rows of m) * b[.][n]^T for the four
-// 16-row blocks m.  `slice`: shared address of this lane's 16 bytes in block row g = lane / 4.
+// One warp's slice of a stage, one of its four blocks of 16 weight rows: acc[n] += A * b[.][n]^T.
+// `slice`: shared address of this lane's 16 bytes in row g = lane / 4 of the first block.
 // PARTS: activations given as a sum of PARTS terms (bf16 h as high and low part).
 template <bool FP8, int NT, int PARTS>
-__device__ __forceinline__ void ws_multiply(uint32_t slice, const uint4 (&b)[PARTS][NT],
-                                            float (&acc)[4][NT][4]) {
-  static_assert(!FP8 || PARTS == 1, "");
-  uint32_t bh[NT][8];
-  if (FP8) {
+__device__ __forceinline__ void ws_multiply(uint32_t slice, int block, const uint4 (&b)[PARTS][NT],
+                                            float (&acc)[NT][4]) {
+  const uint4 lo = lds128(slice + (uint32_t)(block * 16 * 128));
+  const uint4 hi = lds128(slice + (uint32_t)((block * 16 + 8) * 128));
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const uint32_t w[4] = {b[0][n].x, b[0][n].y, b[0][n].z, b[0][n].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bh[n][2 * i] = e4m3x2_to_half2(w[i] & 0xffffu);
-        bh[n][2 * i + 1] = e4m3x2_to_half2(w[i] >> 16);
+      if (FP8) {
+        mma_e4m3(acc[n], lo.x, hi.x, lo.y, hi.y, b[p][n].x, b[p][n].y);
+        mma_e4m3(acc[n], lo.z, hi.z, lo.w, hi.w, b[p][n].z, b[p][n].w);
+      } else {
+        mma_bf16(acc[n], lo.x, hi.x, lo.y, hi.y, b[p][n].x, b[p][n].y);
+        mma_bf16(acc[n], lo.z, hi.z, lo.w, hi.w, b[p][n].z, b[p][n].w);
       }
     }
-  }
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const uint4 lo = lds128(slice + (uint32_t)(m * 16 * 128));
-    const uint4 hi = lds128(slice + (uint32_t)((m * 16 + 8) * 128));
-    if (FP8) {
-      const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t a0 = e4m3x2_to_half2(l[i] & 0xffffu), a2 = e4m3x2_to_half2(l[i] >> 16);
-        const uint32_t a1 = e4m3x2_to_half2(h[i] & 0xffffu), a3 = e4m3x2_to_half2(h[i] >> 16);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma_f16(acc[m][n], a0, a1, a2, a3, bh[n][2 * i], bh[n][2 * i + 1]);
-      }
-    } else {
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma_bf16(acc[m][n], lo.x, hi.x, lo.y, hi.y, b[p][n].x, b[p][n].y);
-          mma_bf16(acc[m][n], lo.z, hi.z, lo.w, hi.w, b[p][n].z, b[p][n].w);
-        }
-    }
-  }
 }
 
 template <int NT>
