@@ -22,8 +22,8 @@ struct moe_plan_s {
       off_ids, off_w, off_perm,
       off_inv, off_rowtok, off_xp, off_sx, off_h, off_sh, off_y;
   // moe_forward_few
-  size_t off_few_logits, off_few_counters, off_few_part, off_few_hf;
-  int few_counters;
+  size_t off_few_logits, off_few_counters, off_few_part, off_few_h, off_few_sh;
+  int few_slots;
   unsigned long long wait_limit_ns;
   int device;
   int num_sms;
@@ -202,14 +202,20 @@ MOE_EXPORT moe_status moe_plan_create(const moe_config* cfg, moe_plan_t* plan,
     p->off_sh = take(sizeof(float) * ((size_t)imax / 128) * r_cap);
     p->off_y = take(2 * r_cap * H);
   }
-  // moe_forward_few: router sums, counters, partial tiles, FP8: h before quantisation
+  // moe_forward_few: router sums, counters, partial tiles, h in rows [slot][token] (bf16: two
+  // parts; FP8: codes and scales)
   const size_t few = T < MOE_FEW_TOKENS_MAX ? T : MOE_FEW_TOKENS_MAX;
-  p->few_counters = 3 * moe::kFewMaxCtas + (int)(few * ks) * (imax / 128);
+  const size_t slots = (E < few * c.top_k_max ? E : few * c.top_k_max) + S;
+  const size_t few_rows = slots * MOE_FEW_TOKENS_MAX;
+  p->few_slots = (int)slots;
   p->off_few_logits =
       take(sizeof(float) * moe::kFewRouterSplits * MOE_FEW_TOKENS_MAX * E);
-  p->off_few_counters = take(sizeof(unsigned int) * (size_t)p->few_counters);
-  p->off_few_part = take(sizeof(float) * moe::kFewMaxCtas * 4 * moe::kWsTileFloats);
-  p->off_few_hf = c.wtype == MOE_W_BF16 ? 0 : take(sizeof(float) * few * ks * (size_t)imax);
+  p->off_few_counters = take(sizeof(unsigned int) * 3 * moe::kFewMaxCtas);
+  p->off_few_part =
+      take(sizeof(float) * moe::kFewMaxCtas * 4 * MOE_FEW_TOKENS_MAX * moe::kWsRows);
+  const bool few_fp8 = c.wtype != MOE_W_BF16;
+  p->off_few_h = take(few_rows * (size_t)imax * (few_fp8 ? 1 : 4));
+  p->off_few_sh = few_fp8 ? take(sizeof(float) * few_rows * (imax / 128)) : 0;
   p->ws_bytes = off;
   p->wait_limit_ns = 2000000000ull;
   p->device = -1;
@@ -548,15 +554,13 @@ MOE_EXPORT moe_status moe_forward_few(moe_plan_t plan, const moe_weights* wts, c
   a.ss_down = wts->ss_down;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.logits = at<float>(workspace, plan->off_few_logits);
-  a.h = at<uint8_t>(workspace, plan->off_h);
-  a.h32 = at<float>(workspace, plan->off_few_hf);
-  a.sh = at<float>(workspace, plan->off_sh);
+  a.h_slots = plan->few_slots;
+  a.h = at<uint8_t>(workspace, plan->off_few_h);
+  a.sh = at<float>(workspace, plan->off_few_sh);
   a.xq = at<uint8_t>(workspace, plan->off_xp);
   a.sx = at<float>(workspace, plan->off_sx);
   a.part = at<float>(workspace, plan->off_few_part);
-  a.counters = a.split_count = at<unsigned int>(workspace, plan->off_few_counters);
-  a.group_count = a.split_count + 3 * moe::kFewMaxCtas;
-  a.n_counters = plan->few_counters;
+  a.split_count = at<unsigned int>(workspace, plan->off_few_counters);
   a.status = at<unsigned int>(workspace, plan->off_status);
   a.bar = a.status + 16;               // beside the status word, cleared with it
   a.timeout_bit = MOE_DEV_WAIT_TIMEOUT_FEW;

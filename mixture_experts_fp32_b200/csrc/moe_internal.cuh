@@ -172,16 +172,13 @@ struct FewArgs {
   // workspace
   float* logits;                 // [router splits][MOE_FEW_TOKENS_MAX][E]
   int router_splits, router_k;   // K splits of the router, values of K in each
-  uint8_t* h;                    // bf16: rows 2r (high part), 2r + 1 (low); FP8: codes of row r
-  float* h32;                    // FP8: h before quantisation [rows][imax]
+  int h_slots;                   // expert slots of h (shared expert first)
+  uint8_t* h;                    // [slot][token][imax] codes; bf16: [slot][high, low][token][imax]
   float* sh;                     // FP8: scales of h
   uint8_t* xq;                   // FP8: codes and scales of x
   float* sx;
-  float* part;                   // partial tiles [CTA][2 ranges][head, tail]
-  unsigned int* counters;        // split_count and group_count together, zeroed by the kernel
-  int n_counters;
-  unsigned int* split_count;     // [3 ranges][kFewMaxCtas]
-  unsigned int* group_count;     // FP8: [S + selected experts][imax / 128]
+  float* part;                   // partial tiles [2 ranges][CTA][head, tail]
+  unsigned int* split_count;     // [3 ranges][kFewMaxCtas], zeroed by the kernel
   unsigned int* bar;             // two grid barriers, zero before the launch
   unsigned int* status;
   unsigned int timeout_bit;

@@ -2,8 +2,7 @@
 //
 //   out[m, n] = sum_kb sa[m, kb] * sw[n / 128, kb] * sum_{k in kb} a[m, k] * w[n, k]
 //
-// Few rows: the weights stream once past 16 rows at a time (weight_stream.cuh); a tile is
-// 64 weight rows, HBM the bound.
+// Up to 32 rows: the weights stream once past all of them (weight_stream.cuh); HBM is the bound.
 #include <string.h>
 
 #include <new>
@@ -22,7 +21,6 @@ namespace moe {
 namespace {
 
 constexpr int kMaxCtas = 160;
-constexpr unsigned long long kDrainNs = 1000000000ull;
 
 struct ProductArgs {
   const uint8_t* a;
@@ -39,179 +37,132 @@ struct ProductArgs {
   unsigned long long wait_limit_ns;
 };
 
-__device__ __forceinline__ void store_out(const ProductArgs& p, int m, int n, float v) {
-  if (p.f32)
-    static_cast<float*>(p.out)[m * p.ldo + n] = v;
-  else
-    static_cast<__nv_bfloat16*>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
+// out[m][n .. n + 3], n a multiple of 4, as far as n < N; one store where it is aligned.
+__device__ __forceinline__ void store_out4(const ProductArgs& p, int m, int n, const float (&v)[4]) {
+  const long long at = m * p.ldo + n;
+  if (p.f32) {
+    float* o = static_cast<float*>(p.out) + at;
+    if (n + 3 < p.N && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < p.N) o[i] = v[i];
+    }
+  } else {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    if (n + 3 < p.N && (reinterpret_cast<uintptr_t>(o) & 7u) == 0) {
+      *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                                *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+      const __nv_bfloat16 h[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < p.N) o[i] = h[i];
+    }
+  }
 }
 
-template <int NT>
+template <int ROWS>
 struct RowsSmem {
-  static constexpr int kStages = NT == 1 ? 6 : 5;
-  alignas(1024) uint8_t ring[kStages * kWsStageBytes];
-  alignas(16) float red[kWsWarps * 8 * NT * kWsRedPitch];
-  uint64_t full[kStages], empty[kStages];
+  WsSmem<ROWS, ROWS, ROWS == 16 ? 6 : 5> ws;          // as many stages as 227 KB hold
   int flag;
 };
 
-template <int NT>
-__global__ void __launch_bounds__(kWsBlock, 1) product_rows_kernel(const __grid_constant__ CUtensorMap wmap,
-                                                                   const ProductArgs p) {
+template <int ROWS>
+__global__ void __launch_bounds__(kWsBlock, 1)
+    product_rows_kernel(const __grid_constant__ CUtensorMap wmap,
+                        const __grid_constant__ CUtensorMap amap, const ProductArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  RowsSmem<NT>& s = *reinterpret_cast<RowsSmem<NT>*>(
+  RowsSmem<ROWS>& s = *reinterpret_cast<RowsSmem<ROWS>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int kStages = RowsSmem<NT>::kStages;
-  constexpr int TT = 8 * NT;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  using S = decltype(s.ws);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
-  const int per = (p.K + kWsBytes - 1) / kWsBytes;            // stages of a tile
+  const int per = p.kb;                               // stages of a tile
   const WsSplit split((p.N + kWsRows - 1) / kWsRows * per, ctas);
-  const int u1 = split.begin(cta + 1);
-  constexpr unsigned int kBit = MOE_DEV_WAIT_TIMEOUT_PRODUCT;
+  const int ub = split.begin(cta), ue = split.begin(cta + 1);
+  const WsRole role{p.wait_limit_ns, p.status, MOE_DEV_WAIT_TIMEOUT_PRODUCT};
+  ws_setup(s.ws);
 
-  if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 1);
-      mbar_init(smem_u32(&s.empty[i]), kWsWarps);
+  if (warp == 1) {
+    WsWeights<S> out(s.ws, role);
+    for (int u = ub; u < ue; ++u) {
+      const int tile = u / per, row = tile * kWsRows;
+      out.load(&wmap, row, row + kWsBoxRows < p.N ? row + kWsBoxRows : -1,
+               (u - tile * per) * kWsBytes);
     }
-    fence_mbarrier_init();
+    out.drain();
+  } else if (warp == 2) {
+    WsMma<true, S> mma(s.ws, role);
+    for (int u = ub; u < ue; ++u) mma.stage(true, true);
+    mma.drain();
+  } else if (warp == 3) {
+    WsActivations<S> out(s.ws, role);
+    for (int u = ub; u < ue; ++u) out.load(&amap, 0, u % per * kWsBytes, ROWS);
+    out.drain();
+  } else {
+    const bool worker = ws_is_worker(warp), promoter = (warp & 3) == 0;
+    const int tid = (int)threadIdx.x - kWsFirst;
+    WsPromoter<S> sum(s.ws, role);
+    for (int u = ub; u < ue;) {
+      const int tile = u / per, c0 = u - tile * per, c1 = min(per, c0 + (ue - u)), t0 = u - c0;
+      u += c1 - c0;
+      if (promoter) {
+        sum.clear();
+        // its columns' row of scale blocks; past the end of N the last one, whose sums are not used
+        const int rb = min(tile * 2 + (threadIdx.x < 256 ? 0 : 1), (p.N - 1) / 128);
+        WsScales w, x;
+        w.reset(p.sw + (size_t)rb * p.kb, p.kb, c0);
+        x.reset(p.sa + (size_t)lane * p.kb, lane < p.M ? p.kb : 0, c0);
+        for (int c = c0; c < c1; ++c) sum.add(w.at(c) * x.at(c), lane < p.M);
+      }
+      ws_tile_free();
+      if (promoter) sum.park(ROWS);
+      ws_tile_ready();
+      if (!worker) continue;
+      int b0 = 0, b1 = 0;
+      if (c1 - c0 < per) {
+        b0 = split.owner(t0);
+        b1 = split.owner(t0 + per - 1);
+        ws_store_partial<ROWS>(s.ws.tile, p.part, cta, b0, p.M);
+        if (!ws_arrive_last(p.counters + b0, b1 - b0 + 1, &s.flag, true)) continue;
+      }
+      // four columns of a row a thread at a time
+      for (int i = tid; i < p.M * (kWsRows / 4); i += kWsThreads) {
+        const int m = i / (kWsRows / 4), col = i % (kWsRows / 4) * 4, n = tile * kWsRows + col;
+        if (n >= p.N) continue;
+        float v[4];
+        ws_tile_values<ROWS>(s.ws.tile[m], p.part, b0, b1, m, col, v);
+        store_out4(p, m, n, v);
+      }
+    }
   }
-  __syncthreads();
-
-  if (warp == kWsWarps) {
-    const uint64_t once = policy_evict_first();
-    int stage = 0;
-    uint32_t phase = 0, issued = 0, parity = 0;
-    for (int u = split.begin(cta); u < u1; ++u) {
-      const int tile = u / per, c = u - tile * per;
-      if (!ws_wait(smem_u32(&s.empty[stage]), phase ^ 1u, p.wait_limit_ns, p.status,
-                                kBit))
-        break;
-      ws_load_stage(smem_u32(s.ring + stage * kWsStageBytes), &wmap, tile * kWsRows,
-                    tile * kWsRows + kWsBoxRows, c * kWsBytes, min(kWsBytes, p.K - c * kWsBytes),
-                    smem_u32(&s.full[stage]), once);
-      issued |= 1u << stage;
-      parity = (parity & ~(1u << stage)) | (phase << stage);
-      if (++stage == kStages) { stage = 0; phase ^= 1u; }
-    }
-    // no copy may still be writing when the CTA leaves
-    for (int i = 0; i < kStages; ++i)
-      if ((issued >> i) & 1u)
-        ws_wait(smem_u32(&s.full[i]), (parity >> i) & 1u, kDrainNs, p.status, kBit);
-    return;
-  }
-
-  const int g = lane >> 2, q = lane & 3;
-  bool ok = true;
-  int stage = 0;
-  uint32_t phase = 0;
-  const uint32_t lane_off = ws_lane_offset(warp, lane);
-  auto sync = []() { named_bar_sync(1, kWsThreads); };
-  for (int u = split.begin(cta); u < u1;) {
-    const int tile = u / per, c0 = u - tile * per, c1 = min(per, c0 + (u1 - u)), t0 = u - c0;
-    u += c1 - c0;
-    const float* sw = p.sw + (size_t)(tile * kWsRows / 128) * p.kb;
-    struct Frag {
-      uint4 b[1][NT];
-      float fa[NT][2], fw;                    // multiplied where they are used: loads stay ahead
-    };
-    auto fetch = [&](int c, Frag& x) {
-      const int k = c * kWsBytes + warp * 64;
-      const bool live = k + q * 16 < p.K;     // K may end inside the slice
-      x.fw = k < p.K ? __ldg(sw + k / 128) : 0.f;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        x.b[0][n] = make_uint4(0, 0, 0, 0);
-        if (live && n * 8 + g < p.M)
-          x.b[0][n] =
-              __ldg(reinterpret_cast<const uint4*>(p.a + (size_t)(n * 8 + g) * p.K + k + q * 16));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = n * 8 + 2 * q + i;
-          x.fa[n][i] = k < p.K && t < p.M ? __ldg(p.sa + (size_t)t * p.kb + k / 128) : 0.f;
-        }
-      }
-    };
-    float acc[4][NT][4];
-    ws_zero<NT>(acc);
-    // fragments of two stages are under way while a third is multiplied
-    Frag x[3];
-    fetch(c0, x[0]);
-    if (c0 + 1 < c1) fetch(c0 + 1, x[1]);
-    for (int c = c0; c < c1; c += 3) {
-#pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        if (c + j >= c1) break;
-        if (c + j + 2 < c1) fetch(c + j + 2, x[(j + 2) % 3]);
-        if (ok) ok = ws_wait(smem_u32(&s.full[stage]), phase, p.wait_limit_ns, p.status, kBit);
-        if (ok && (c + j) * kWsBytes + warp * 64 < p.K) {
-          const uint32_t slice = smem_u32(s.ring + stage * kWsStageBytes) + lane_off;
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            float part[NT][4] = {};
-            ws_multiply<true, NT, 1>(slice, m, x[j].b, part);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                acc[m][n][i] = fmaf(part[n][i], x[j].fw * x[j].fa[n][i & 1], acc[m][n][i]);
-          }
-        }
-        __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(smem_u32(&s.empty[stage]));
-        if (++stage == kStages) { stage = 0; phase ^= 1u; }
-      }
-    }
-    ws_park<NT>(s.red, warp, lane, acc);
-    sync();
-    bool finish = true;
-    const bool shared = c1 - c0 < per;
-    const int b0 = split.owner(t0), b1 = split.owner(t0 + per - 1);
-    if (shared) {
-      for (int i = tid; i < TT * 32; i += kWsThreads) {
-        const int t = i >> 5, r = (i & 31) * 2;
-        *reinterpret_cast<float2*>(ws_partial(p.part, cta, b0) + t * kWsRows + r) = ws_sum<NT>(s.red, t, r);
-      }
-      sync();
-      if (tid == 0) {
-        __threadfence();
-        s.flag = atomicAdd(p.counters + b0, 1u) == (unsigned int)(b1 - b0);
-        if (s.flag) p.counters[b0] = 0;               // as the next launch expects it
-        __threadfence();
-      }
-      sync();
-      finish = s.flag != 0;
-    }
-    if (finish) {
-      for (int i = tid; i < TT * 32; i += kWsThreads) {
-        const int t = i >> 5, r = (i & 31) * 2, n = tile * kWsRows + r;
-        if (t >= p.M || n >= p.N) continue;
-        const float2 v = shared ? ws_joined(p.part, b0, b1, t, r) : ws_sum<NT>(s.red, t, r);
-        store_out(p, t, n, v.x);
-        if (n + 1 < p.N) store_out(p, t, n + 1, v.y);
-      }
-    }
-    sync();                                           // red and flag are free again
-  }
+  ws_teardown(s.ws);
 }
 
-template <int NT>
-cudaError_t launch_rows(const CUtensorMap& m, const ProductArgs& a, int ctas, cudaStream_t st) {
-  product_rows_kernel<NT><<<ctas, kWsBlock, sizeof(RowsSmem<NT>) + 1024, st>>>(m, a);
+template <int ROWS>
+cudaError_t launch_rows(const CUtensorMap& w, const ProductArgs& a, int ctas, cudaStream_t st) {
+  CUtensorMap am;
+  if (!ws_map(&am, a.a, a.K, a.M, ROWS)) return cudaErrorInvalidValue;
+  product_rows_kernel<ROWS><<<ctas, kWsBlock, sizeof(RowsSmem<ROWS>) + 1024, st>>>(w, am, a);
   return cudaGetLastError();
+}
+
+template <int ROWS>
+cudaError_t prepare_rows() {
+  static_assert(sizeof(RowsSmem<ROWS>) + 1024 <= 227 * 1024, "shared memory of one CTA");
+  return cudaFuncSetAttribute(product_rows_kernel<ROWS>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)sizeof(RowsSmem<ROWS>) + 1024);
 }
 
 }  // namespace
 
 cudaError_t prepare_product_kernels() {
-  cudaError_t e = cudaFuncSetAttribute(product_rows_kernel<1>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(RowsSmem<1>) + 1024);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(product_rows_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sizeof(RowsSmem<2>) + 1024);
-  return e;
+  const cudaError_t e = prepare_rows<16>();
+  return e == cudaSuccess ? prepare_rows<32>() : e;
 }
 
 }  // namespace moe
@@ -230,7 +181,8 @@ MOE_EXPORT moe_status moe_product_create(const moe_product_config* cfg, moe_prod
   p->cfg = *cfg;
   p->off_counters = 256;
   p->off_part = 256 + 1024;
-  p->ws_bytes = p->off_part + sizeof(float) * 2 * moe::kMaxCtas * moe::kWsTileFloats;
+  p->ws_bytes = p->off_part + sizeof(float) * 2 * moe::kMaxCtas * moe::kWsRows *
+                                  (size_t)(cfg->max_rows <= 16 ? 16 : 32);
   p->wait_limit_ns = 2000000000ull;
   *product = p;
   *workspace_bytes = p->ws_bytes;
@@ -281,15 +233,16 @@ MOE_EXPORT moe_status moe_block_scaled_product(moe_product_t p, const void* a,
   g.status = reinterpret_cast<unsigned int*>(ws);
   g.wait_limit_ns = p->wait_limit_ns;
   const int ctas = sms < moe::kMaxCtas ? sms : moe::kMaxCtas;
-  CUtensorMap wmap;
-  if (!moe::ws_weight_map(&wmap, w, g.K, g.N)) return moe::cuda_status(cudaErrorInvalidValue);
-  for (int m0 = 0; m0 < rows && s == MOE_OK; m0 += 16) {
-    g.M = rows - m0 < 16 ? rows - m0 : 16;
+  CUtensorMap wm;
+  if (!moe::ws_map(&wm, w, g.K, g.N, moe::kWsBoxRows))
+    return moe::cuda_status(cudaErrorInvalidValue);
+  for (int m0 = 0; m0 < rows && s == MOE_OK; m0 += 32) {
+    g.M = rows - m0 < 32 ? rows - m0 : 32;
     g.a = static_cast<const uint8_t*>(a) + (size_t)m0 * g.K;
     g.sa = a_scales + (size_t)m0 * g.kb;
     g.out = static_cast<uint8_t*>(out) + (size_t)m0 * ldo * (f32 ? 4 : 2);
-    s = moe::cuda_status(g.M <= 8 ? moe::launch_rows<1>(wmap, g, ctas, st)
-                                  : moe::launch_rows<2>(wmap, g, ctas, st));
+    s = moe::cuda_status(g.M <= 16 ? moe::launch_rows<16>(wm, g, ctas, st)
+                                   : moe::launch_rows<32>(wm, g, ctas, st));
   }
   return s;
 }

@@ -1,50 +1,67 @@
 // Streaming a weight matrix past a few activation rows: the pieces shared by the
 // few-token layer and the block-scaled product of few rows.
 //
-// Both read every weight once and multiply it with at most 8 * NT activation rows, so
-// they are bound by HBM, not by arithmetic: at 6.5 TB/s an SM receives about 23 bytes of
-// weights a clock, one m16n8k16 product every 22 clocks.  That decides the form:
-//  - weights travel by TMA into a ring of stages in shared memory (64 weight rows x 512
-//    bytes of K each, eight boxes of 32 rows x 128 bytes), which keeps 160 KB or more a CTA
-//    in flight whatever the consumers do and runs on across tiles, barriers and phases.
-//    (Bulk copies of 512-byte row segments, which need no tensor map, brought 1.9 TB/s;)
-//  - eight warps consume a stage, each a 64-byte slice of K of all 64 rows, as the A
-//    operand (weights on the M side, activation rows on the N side) of warp-wide m16n8
-//    products (k16 bf16, k32 e4m3).  The order of K inside a slice does not matter as long as both
-//    operands agree, so lane (g, q) takes 16 contiguous bytes of rows g and g + 8: one
-//    128-bit shared load per row feeds two products, and the
-//    activation fragment is 16 contiguous bytes of its row, read straight from L2.
-//    tcgen05 would need 128-row tiles, accumulators in tensor memory and a round trip
-//    through it for every scale group, to save arithmetic that is not the bound;
-//  - the eight partial sums of a tile meet in shared memory once per tile.
+// Both read every weight once and multiply it with 32 activation rows at most, so they are
+// bound by HBM, not by arithmetic: at 6.5 TB/s an SM receives about 23 bytes of weights a
+// clock, 256 rows x 128 bytes of K every 1400 clocks.  What matters is that nothing else
+// takes longer than that, and that loads never pause:
+//  - weights travel by TMA into a ring of stages in shared memory (256 weight rows x 128
+//    bytes of K, two boxes of 128 rows), 160 KB or more a CTA in flight, by a producer that
+//    runs on across tiles, barriers and phases;
+//  - tcgen05 multiplies straight from shared memory, so that no instruction handles a
+//    single weight, with the weights on the N side (256) and the few activation rows on the
+//    M side (128, of which the rest is whatever lies behind them in shared memory: rows of
+//    a product do not meet).  An MMA of 128 rows took 130 (bf16) to 220 (e4m3) clocks
+//    whatever its N, so weights on the M side would pass at 31 or 19 bytes a clock; the
+//    same product with warp-wide mma.sync took 330 instructions a warp and stage;
+//  - a second producer brings the activation rows, so that weights can be under way before
+//    the activations they will meet have been computed;
+//  - block scales change every 128 bytes of K (FP8): each stage is multiplied into one of
+//    two tensor-memory buffers, and four promoter warps (the ones that can read the first
+//    32 lanes, 64 columns each) add it to their fp32 sums with its scale.  Otherwise a
+//    buffer takes a whole run of K.
 //
 // Work is cut into units of one stage.  Each CTA takes a contiguous range of the units
 // (within one unit of an even split, whatever the shapes); a tile whose units fall to
-// several CTAs is finished by the last of them to arrive, which adds the others'
-// partial tiles from global memory in CTA order, so results do not depend on timing.
+// several CTAs is finished by the last of them to arrive, which adds the partial tiles
+// from global memory in CTA order, so results do not depend on timing.
+//
+// Thirteen warps: 1 weight producer, 2 MMA issuer, 3 activation producer; promoters 0, 4, 8,
+// 12 (lane: activation row; warp / 4: columns, i.e. weight rows, 64 (warp / 4) .. + 63);
+// workers 4 .. 11, who take a finished tile from shared memory.
 #pragma once
 
 #include "moe_internal.cuh"
 
 namespace moe {
 
-constexpr int kWsRows = 64;                   // weight rows of a stage
-constexpr int kWsBytes = 512;                 // bytes of K of a stage
-constexpr int kWsBoxRows = 32;                // a box: 32 rows x 128 bytes, 128-byte swizzle
-constexpr int kWsBoxBytes = kWsBoxRows * 128;
-constexpr int kWsColumn = kWsRows * 128;      // 128 bytes of K of all 64 rows: two boxes
+constexpr int kWsRows = 256;                  // weight rows of a tile
+constexpr int kWsBytes = 128;                 // bytes of K of a stage
+constexpr int kWsBoxRows = 128;               // rows of a TMA box of weights
 constexpr int kWsStageBytes = kWsRows * kWsBytes;
-constexpr int kWsWarps = 8;                   // consumers; warp w takes bytes 64w .. 64w + 63
-constexpr int kWsThreads = kWsWarps * 32;     // consumer threads
-constexpr int kWsBlock = kWsThreads + 32;     // and one producer warp
-// partial sums of a tile in shared memory: [warp][activation row][weight row], rows of 68
-// floats so that the fragments' stores are free of bank conflicts
-constexpr int kWsRedPitch = 68;
-constexpr int kWsTileFloats = 16 * kWsRows;   // a partial tile in global memory, 16 rows
+constexpr int kWsWorkers = 8;                 // warps
+constexpr int kWsThreads = kWsWorkers * 32;   // worker threads
+constexpr int kWsFirst = 128;                 // first worker thread
+constexpr int kWsBlock = 13 * 32;
+constexpr int kWsCols = kWsRows / 4;          // columns of a promoter
+constexpr int kWsTilePitch = kWsRows + 4;     // a finished tile in shared memory: rows apart
+constexpr unsigned long long kWsDrainNs = 1000000000ull;
 
-// Tensor map of a row-major weight matrix [rows, row_bytes] in boxes of 32 rows x 128 bytes;
-// what lies past its end reads as zero.
-bool ws_weight_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64_t rows);
+// Shared memory of the stream.  ROWS: activation rows brought (16 or 32), TILE: rows of a
+// finished tile.
+template <int ROWS_, int TILE, int STAGES_>
+struct WsSmem {
+  static constexpr int ROWS = ROWS_, STAGES = STAGES_;
+  alignas(1024) uint8_t x[STAGES][ROWS * kWsBytes];   // MMAs read 128 rows from here: into w
+  alignas(1024) uint8_t w[STAGES][kWsStageBytes];
+  alignas(16) float tile[TILE][kWsTilePitch];
+  uint64_t full_w[STAGES], full_x[STAGES], empty[STAGES], dfull[2], dempty[2], teardown;
+  uint32_t tmem;
+};
+
+// Tensor map of a row-major matrix [rows, row_bytes] in boxes of box_rows x 128 bytes with
+// the 128-byte swizzle; what lies past its end reads as zero.
+bool ws_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64_t rows, int box_rows);
 
 #if defined(__CUDACC__)
 
@@ -61,30 +78,12 @@ struct WsSplit {
   }
 };
 
-// A tile that several CTAs share: CTA b's partial tile.  The first of them ends inside the
-// tile (its tail), the others begin inside it (their head); part: [CTA][head, tail].
+// A tile that several CTAs share: CTA b's partial tile [ROWS][kWsRows].  The first of them
+// ends inside the tile (its tail), the others begin inside it (their head); part: [CTA][head,
+// tail].
+template <int ROWS>
 __device__ __forceinline__ float* ws_partial(float* part, int b, int first) {
-  return part + (size_t)(b * 2 + (b == first ? 1 : 0)) * kWsTileFloats;
-}
-
-// Sum over CTAs b0 .. b1, in that order, of weight rows r, r + 1 of activation row t of their
-// partial tiles; the loads of eight CTAs go out together.
-__device__ __forceinline__ float2 ws_joined(float* part, int b0, int b1, int t, int r) {
-  float2 v = make_float2(0.f, 0.f);
-  for (int b = b0; b <= b1; b += 8) {
-    float2 o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      o[i] = b + i <= b1 ? __ldcg(reinterpret_cast<const float2*>(
-                               ws_partial(part, b + i, b0) + t * kWsRows + r))
-                         : make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v.x += o[i].x;
-      v.y += o[i].y;
-    }
-  }
-  return v;
+  return part + (size_t)(b * 2 + (b == first ? 1 : 0)) * (ROWS * kWsRows);
 }
 
 // Bounded wait taken by a whole warp (warp-uniform result): a limit of 0 gives up at once
@@ -103,118 +102,317 @@ __device__ __forceinline__ bool ws_wait(uint32_t bar, uint32_t parity, unsigned 
     if ((threadIdx.x & 31) == 0) atomicOr(status, bit);
     return false;
   }
-  return mbar_wait_sleep_warp(bar, parity, limit_ns, status, bit);
+  return mbar_wait_bounded_warp(bar, parity, limit_ns, status, bit);
 }
 
-// One stage by a warp: bytes [koff, koff + bytes) of K of weight rows row0 .. + 31 and
-// row1 .. + 31, a box a lane; `bytes` beyond a multiple of 128 arrive as zeros.
-__device__ __forceinline__ void ws_load_stage(uint32_t dst, const CUtensorMap* m, int row0,
-                                              int row1, int koff, int bytes, uint32_t bar,
-                                              uint64_t policy) {
-  const int lane = threadIdx.x & 31;
-  const int columns = (bytes + 127) / 128;
-  if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(columns * kWsColumn));
+// A place in a ring of n slots.
+struct WsPos {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) { i = 0; phase ^= 1u; }
+  }
+};
+
+// What a role of the stream carries: its waits, and whether one of them has run out.
+struct WsRole {
+  unsigned long long limit_ns;
+  unsigned int* status;
+  unsigned int bit;
+  bool ok = true;
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    if (ok) ok = ws_wait(smem_u32(bar), parity, limit_ns, status, bit);
+    return ok;
+  }
+};
+
+// Before the roles part, by all threads (ends in a block barrier).
+template <class S>
+__device__ __forceinline__ void ws_setup(S& s) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::STAGES; ++i) {
+      mbar_init(smem_u32(&s.full_w[i]), 1);
+      mbar_init(smem_u32(&s.full_x[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.dfull[i]), 1);
+      mbar_init(smem_u32(&s.dempty[i]), 4);
+    }
+    mbar_init(smem_u32(&s.teardown), 1);
+    fence_mbarrier_init();
+  }
+  if ((threadIdx.x >> 5) == 2) {
+    tmem_alloc(smem_u32(&s.tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+
+// After the roles have finished, by all threads.
+template <class S>
+__device__ __forceinline__ void ws_teardown(S& s) {
   __syncwarp();
-  if (lane < 2 * columns)
-    tma_load_2d(dst + lane * kWsBoxBytes, m, koff + (lane >> 1) * 128, (lane & 1) ? row1 : row0,
-                bar, policy);
+  tc_fence_before();
+  __syncthreads();
+  if ((threadIdx.x >> 5) == 2) {
+    tc_fence_after();
+    tmem_dealloc(s.tmem, 512);
+  }
 }
 
-// Weight row (of a block of 8) that fragment row g holds: rows 4 apart for neighbouring g,
-// so that the 16-byte chunks of a quarter-warp, which the swizzle moves by the row's low
-// three bits, fall on all 32 banks.
-__device__ __forceinline__ int ws_row(int g) { return (g >> 1) | ((g & 1) << 2); }
+// Weight producer (one warp): a stage holds 128 bytes of K at koff (what lies past the rows'
+// end arrives as zeros) of weight rows row0 .. + 127 and, unless row1 < 0, row1 .. + 127.
+template <class S>
+struct WsWeights {
+  S& s;
+  WsRole role;
+  WsPos pos;
+  uint64_t policy = policy_evict_first();     // weights are read once
+  uint32_t issued = 0, parity = 0;
+  __device__ WsWeights(S& s_, const WsRole& r) : s(s_), role(r) {}
+  __device__ __forceinline__ void load(const CUtensorMap* m, int row0, int row1, int koff) {
+    if (!role.wait(&s.empty[pos.i], pos.phase ^ 1u)) return;
+    if ((threadIdx.x & 31) == 0) {
+      const uint32_t bar = smem_u32(&s.full_w[pos.i]), dst = smem_u32(s.w[pos.i]);
+      mbar_arrive_expect_tx(bar, row1 >= 0 ? kWsStageBytes : kWsStageBytes / 2);
+      tma_load_2d(dst, m, koff, row0, bar, policy);
+      if (row1 >= 0) tma_load_2d(dst + kWsStageBytes / 2, m, koff, row1, bar, policy);
+    }
+    issued |= 1u << pos.i;
+    parity = (parity & ~(1u << pos.i)) | (pos.phase << pos.i);
+    pos.next(S::STAGES);
+  }
+  // no copy may still be writing when the CTA leaves
+  __device__ __forceinline__ void drain() {
+    for (int i = 0; i < S::STAGES; ++i)
+      if ((issued >> i) & 1u)
+        ws_wait(smem_u32(&s.full_w[i]), (parity >> i) & 1u, kWsDrainNs, role.status, role.bit);
+  }
+};
 
-// Offset in a stage of a lane's 16 bytes of fragment row g = lane / 4 of the first block.
-__device__ __forceinline__ uint32_t ws_lane_offset(int warp, int lane) {
-  const int r = ws_row(lane >> 2), chunk = (warp & 1) * 4 + (lane & 3);
-  return (uint32_t)((warp >> 1) * kWsColumn + r * 128 + (chunk ^ r) * 16);
-}
+// Activation producer (one warp): the same 128 bytes of K of activation rows row .. + ROWS - 1.
+template <class S>
+struct WsActivations {
+  S& s;
+  WsRole role;
+  WsPos pos;
+  uint64_t policy = policy_evict_last();      // and read again by every CTA
+  uint32_t issued = 0, parity = 0;
+  __device__ WsActivations(S& s_, const WsRole& r) : s(s_), role(r) {}
+  __device__ __forceinline__ void load(const CUtensorMap* m, int row, int koff, int box_rows) {
+    if (!role.wait(&s.empty[pos.i], pos.phase ^ 1u)) return;
+    if ((threadIdx.x & 31) == 0) {
+      const uint32_t bar = smem_u32(&s.full_x[pos.i]);
+      mbar_arrive_expect_tx(bar, box_rows * kWsBytes);
+      tma_load_2d(smem_u32(s.x[pos.i]), m, koff, row, bar, policy);
+    }
+    issued |= 1u << pos.i;
+    parity = (parity & ~(1u << pos.i)) | (pos.phase << pos.i);
+    pos.next(S::STAGES);
+  }
+  __device__ __forceinline__ void drain() {
+    for (int i = 0; i < S::STAGES; ++i)
+      if ((issued >> i) & 1u)
+        ws_wait(smem_u32(&s.full_x[i]), (parity >> i) & 1u, kWsDrainNs, role.status, role.bit);
+  }
+};
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// One warp's slice of a stage, one of its four blocks of 16 weight rows: acc[n] += A * b[.][n]^T.
-// `slice`: shared address of this lane's 16 bytes in row g = lane / 4 of the first block.
-// PARTS: activations given as a sum of PARTS terms (bf16 h as high and low part).
-template <bool FP8, int NT, int PARTS>
-__device__ __forceinline__ void ws_multiply(uint32_t slice, int block, const uint4 (&b)[PARTS][NT],
-                                            float (&acc)[NT][4]) {
-  const uint4 lo = lds128(slice + (uint32_t)(block * 16 * 128));
-  const uint4 hi = lds128(slice + (uint32_t)((block * 16 + 8) * 128));
+// MMA issuer (one warp in step, one lane issues): stages from `begin` to `end` share a buffer.
+template <bool FP8, class S>
+struct WsMma {
+  S& s;
+  WsRole role;
+  WsPos pos, d;
+  bool any = false;
+  __device__ WsMma(S& s_, const WsRole& r) : s(s_), role(r) {}
+  __device__ __forceinline__ void stage(bool begin, bool end) {
+    role.wait(&s.full_w[pos.i], pos.phase);
+    role.wait(&s.full_x[pos.i], pos.phase);
+    if (begin) role.wait(&s.dempty[d.i], d.phase ^ 1u);
+    if (!role.ok) return;
+    tc_fence_after();
+    if ((threadIdx.x & 31) == 0) {
+      const uint32_t dst = s.tmem + d.i * kWsRows;
+      const uint64_t a = smem_desc_sw128(smem_u32(s.x[pos.i]));
+      const uint64_t b = smem_desc_sw128(smem_u32(s.w[pos.i]));
 #pragma unroll
-  for (int p = 0; p < PARTS; ++p)
+      for (int k = 0; k < 4; ++k) {           // 32 bytes of K an instruction
+        if (FP8)
+          umma_e4m3(dst, a + 2 * k, b + 2 * k, idesc_e4m3_m128(kWsRows), k > 0 || !begin);
+        else
+          umma_bf16(dst, a + 2 * k, b + 2 * k, idesc_bf16_m128(kWsRows), k > 0 || !begin);
+      }
+      umma_commit(smem_u32(&s.empty[pos.i]));
+      if (end) umma_commit(smem_u32(&s.dfull[d.i]));
+    }
+    if (end) d.next(2);
+    any = true;
+    pos.next(S::STAGES);
+    __syncwarp();
+  }
+  // the tensor core has finished before tensor memory is freed
+  __device__ __forceinline__ void drain() {
+    if (!any) return;
+    if ((threadIdx.x & 31) == 0) umma_commit(smem_u32(&s.teardown));
+    __syncwarp();
+    ws_wait(smem_u32(&s.teardown), 0, kWsDrainNs, role.status, role.bit);
+  }
+};
+
+// Promoter warp: fp32 sums of its 64 columns of its lane's activation row.
+template <class S>
+struct WsPromoter {
+  S& s;
+  WsRole role;
+  WsPos d;
+  float acc[kWsCols];
+  __device__ WsPromoter(S& s_, const WsRole& r) : s(s_), role(r) {}
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (FP8) {
-        mma_e4m3(acc[n], lo.x, hi.x, lo.y, hi.y, b[p][n].x, b[p][n].y);
-        mma_e4m3(acc[n], lo.z, hi.z, lo.w, hi.w, b[p][n].z, b[p][n].w);
-      } else {
-        mma_bf16(acc[n], lo.x, hi.x, lo.y, hi.y, b[p][n].x, b[p][n].y);
-        mma_bf16(acc[n], lo.z, hi.z, lo.w, hi.w, b[p][n].z, b[p][n].w);
+    for (int i = 0; i < kWsCols; ++i) acc[i] = 0.f;
+  }
+  // acc += f * the next buffer, in lanes that `take` it; the buffer goes back as soon as it
+  // has been read
+  __device__ __forceinline__ void add(float f, bool take) {
+    if (role.wait(&s.dfull[d.i], d.phase)) {
+      tc_fence_after();
+      const uint32_t at = s.tmem + d.i * kWsRows + (threadIdx.x >> 7) * kWsCols;
+#pragma unroll
+      for (int c = 0; c < kWsCols; c += 32) {
+        float v[32];
+        tmem_ld_32(at + c, v);
+        if (c + 32 == kWsCols) {
+          tc_fence_before();
+          __syncwarp();
+          if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&s.dempty[d.i]));
+        }
+        if (take) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(v[i], f, acc[c + i]);
+        }
       }
     }
-}
-
-template <int NT>
-__device__ __forceinline__ void ws_zero(float (&a)[4][NT][4]) {
-#pragma unroll
-  for (int m = 0; m < 4; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[m][n][i] = 0.f;
-}
-
-// A warp's accumulators into its part of the shared partial sums.
-template <int NT>
-__device__ __forceinline__ void ws_park(float* red, int warp, int lane,
-                                        const float (&acc)[4][NT][4]) {
-  const int r = ws_row(lane >> 2), q = lane & 3;
-  float* w = red + warp * (8 * NT * kWsRedPitch);
-#pragma unroll
-  for (int m = 0; m < 4; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[(n * 8 + 2 * q + (i & 1)) * kWsRedPitch + m * 16 + r + 8 * (i >> 1)] = acc[m][n][i];
-}
-
-// Sum over the warps, in warp order, of weight rows r, r + 1 of activation row t.
-template <int NT>
-__device__ __forceinline__ float2 ws_sum(const float* red, int t, int r) {
-  float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < kWsWarps; ++w) {
-    const float2 v =
-        *reinterpret_cast<const float2*>(red + (w * 8 * NT + t) * kWsRedPitch + r);
-    s.x += v.x;
-    s.y += v.y;
+    d.next(2);
   }
-  return s;
+  // the finished sums into the shared tile, rows 0 .. rows - 1
+  __device__ __forceinline__ void park(int rows) {
+    const int lane = threadIdx.x & 31;
+    if (lane < rows) {
+      float4* o = reinterpret_cast<float4*>(&s.tile[lane][(threadIdx.x >> 7) * kWsCols]);
+#pragma unroll
+      for (int i = 0; i < kWsCols / 4; ++i)
+        o[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    }
+  }
+};
+
+// Scales of consecutive K blocks from a row of them (a row a lane, or one for all): four in
+// use, four under way.
+struct WsScales {
+  const float* row = nullptr;
+  int n = 0, base = 0;
+  float cur[4], nxt[4];
+  __device__ __forceinline__ void fetch(int kb, float (&o)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = kb + i < n ? __ldcg(row + kb + i) : 0.f;
+  }
+  // scales of blocks kb, kb + 1, ..; n = 0: none
+  __device__ __forceinline__ void reset(const float* r, int blocks, int kb) {
+    row = r;
+    n = blocks;
+    base = kb;
+    fetch(kb, cur);
+    fetch(kb + 4, nxt);
+  }
+  // that of block kb, which grows by one from call to call
+  __device__ __forceinline__ float at(int kb) {
+    if (kb == base + 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+      base = kb;
+      fetch(kb + 4, nxt);
+    }
+    const int i = kb - base;
+    return i == 0 ? cur[0] : i == 1 ? cur[1] : i == 2 ? cur[2] : cur[3];
+  }
+};
+
+__device__ __forceinline__ bool ws_is_worker(int warp) { return warp >= 4 && warp < 12; }
+__device__ __forceinline__ void ws_workers_sync() { named_bar_sync(1, kWsThreads); }
+// promoters and workers: the shared tile may be written / has been written
+__device__ __forceinline__ void ws_tile_free() { named_bar_sync(2, kWsThreads + 64); }
+__device__ __forceinline__ void ws_tile_ready() { named_bar_sync(3, kWsThreads + 64); }
+
+// Several CTAs share something: true, for all workers, in the CTA that arrives last.  What the
+// others' workers stored before is visible after.
+__device__ __forceinline__ bool ws_arrive_last(unsigned int* counter, unsigned int expected,
+                                               int* flag, bool reset) {
+  ws_workers_sync();
+  if (threadIdx.x == kWsFirst) {
+    __threadfence();
+    const bool last = atomicAdd(counter, 1u) + 1 == expected;
+    if (last && reset) *counter = 0;
+    *flag = last;
+    __threadfence();
+  }
+  ws_workers_sync();
+  return *flag != 0;
+}
+
+// The workers' view of a finished tile: value (row, col) and up to V - 1 behind it, from the
+// shared tile or, where several CTAs share the tile, summed over their partial tiles in CTA
+// order.
+template <int ROWS, int V>
+__device__ __forceinline__ void ws_tile_values(const float* tile_row, float* part, int b0, int b1,
+                                               int row, int col, float (&v)[V]) {
+  static_assert(V % 4 == 0, "");
+  if (b0 == b1) {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const float4 o = *reinterpret_cast<const float4*>(tile_row + col + 4 * i);
+      v[4 * i] = o.x; v[4 * i + 1] = o.y; v[4 * i + 2] = o.z; v[4 * i + 3] = o.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = 0.f;
+  for (int b = b0; b <= b1; b += 4) {
+    float4 o[4][V / 4];                       // the loads of four CTAs go out together
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i)
+        o[j][i] = b + j <= b1 ? __ldcg(reinterpret_cast<const float4*>(
+                                    ws_partial<ROWS>(part, b + j, b0) + row * kWsRows + col) + i)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        v[4 * i] += o[j][i].x; v[4 * i + 1] += o[j][i].y;
+        v[4 * i + 2] += o[j][i].z; v[4 * i + 3] += o[j][i].w;
+      }
+  }
+}
+
+// This CTA's share of a tile from shared memory to its partial tile.
+template <int ROWS>
+__device__ __forceinline__ void ws_store_partial(const float (*tile)[kWsTilePitch], float* part,
+                                                 int cta, int b0, int rows) {
+  float* o = ws_partial<ROWS>(part, cta, b0);
+  for (int i = threadIdx.x - kWsFirst; i < rows * (kWsRows / 4); i += kWsThreads) {
+    const int row = i / (kWsRows / 4), c = i % (kWsRows / 4);
+    reinterpret_cast<float4*>(o + row * kWsRows)[c] =
+        reinterpret_cast<const float4*>(tile[row])[c];
+  }
+}
+
+// Generic-proxy stores to global memory before, bulk (async-proxy) loads of them after.
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async;" ::: "memory");
 }
 
 #endif  // __CUDACC__
