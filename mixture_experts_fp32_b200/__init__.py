@@ -193,6 +193,16 @@ _WEIGHT = ("bfloat16", "uint8", "float8_e4m3fn")
 _CODES = ("uint8", "float8_e4m3fn")
 
 
+_dtype_names: dict = {}          # torch dtype -> its name without "torch."
+
+
+def _dtype_name(dtype) -> str:
+    name = _dtype_names.get(dtype)
+    if name is None:
+        name = _dtype_names[dtype] = str(dtype).rsplit(".", 1)[-1]
+    return name
+
+
 def _addr(t, name: str = "argument", dtypes=None) -> int | None:
     """Address of a tensor argument, or an int taken as a raw address, or None.
 
@@ -208,7 +218,7 @@ def _addr(t, name: str = "argument", dtypes=None) -> int | None:
         raise ValueError(f"{name}: a CUDA tensor is required, got one on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous tensor is required")
-    if dtypes is not None and str(t.dtype).rsplit(".", 1)[-1] not in dtypes:
+    if dtypes is not None and _dtype_name(t.dtype) not in dtypes:
         raise ValueError(f"{name}: element type {t.dtype} is not one of {', '.join(dtypes)}")
     return t.data_ptr()
 
@@ -216,7 +226,7 @@ def _addr(t, name: str = "argument", dtypes=None) -> int | None:
 def _stream(s) -> int | None:
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -355,13 +365,13 @@ def moe_forward_few(plan, weights: moe_weights, hidden, valid, T: int, k: int, o
     _check(st, "moe_forward_few")
 
 
-def _on_one_device(**tensors):
+def _on_current_device(tensors) -> None:
     """Every tensor on the current device: the library launches there."""
     import torch
-    cur = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda and t.device.index != cur:
-            raise ValueError(f"{name}: on {t.device}, the current device is cuda:{cur}")
+    cur = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != cur:
+            raise ValueError(f"a tensor on {t.device}, while the current device is cuda:{cur}")
 
 
 def _rows_of(t, name: str, dtypes) -> tuple[int, int]:
@@ -369,7 +379,7 @@ def _rows_of(t, name: str, dtypes) -> tuple[int, int]:
     the rows themselves may lie further apart, as in a slice of a wider tensor."""
     if not t.is_cuda:
         raise ValueError(f"{name}: a CUDA tensor is required, got one on {t.device}")
-    if str(t.dtype).rsplit(".", 1)[-1] not in dtypes:
+    if _dtype_name(t.dtype) not in dtypes:
         raise ValueError(f"{name}: element type {t.dtype} is not one of {', '.join(dtypes)}")
     rows, cols = t.shape
     if cols > 1 and t.stride(1) != 1:
@@ -402,7 +412,7 @@ def moe_quantize_groups(x, codes, scales, valid=None, gated: bool = False, strea
     addr, ld = _rows_of(x, "x", _BF16 + _F32)
     c, s, v = (_addr(codes, "codes", _CODES), _addr(scales, "scales", _F32),
                _addr(valid, "valid", _MASK))
-    _on_one_device(x=x, codes=codes, scales=scales, valid=valid)
+    _on_current_device((x, codes, scales, valid))
     _check(load().moe_quantize_groups(addr, MOE_T_FP32 if x.element_size() == 4 else MOE_T_BF16,
                                       rows, cols, ld, int(bool(gated)), v, c, s, _stream(stream)),
            "moe_quantize_groups")
@@ -496,7 +506,7 @@ def _host_addr(t, name: str, dtypes=None) -> int | None:
         raise ValueError(f"{name}: a host tensor is required, got one on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous tensor is required")
-    if dtypes is not None and str(t.dtype).rsplit(".", 1)[-1] not in dtypes:
+    if dtypes is not None and _dtype_name(t.dtype) not in dtypes:
         raise ValueError(f"{name}: element type {t.dtype} is not one of {', '.join(dtypes)}")
     return t.data_ptr()
 
@@ -631,7 +641,7 @@ class Plan:
     def forward_few(self, weights: moe_weights, hidden, valid, k: int, out, stream=None, dbg=None):
         """``forward`` for at most MOE_FEW_TOKENS_MAX tokens, in one kernel."""
         T = self._rows(hidden, valid, out)
-        _on_one_device(hidden=hidden, valid=valid, out=out, workspace=self.workspace)
+        _on_current_device((hidden, valid, out, self.workspace))
         moe_forward_few(self.handle, weights, hidden, valid, T, k, out, self.workspace,
                         self.ws_bytes, stream, dbg)
 
@@ -698,29 +708,32 @@ class Product:
         self.handle = None
         if out_dtype not in types:
             raise ValueError(f"out_dtype: {out_dtype} is neither bfloat16 nor float32")
-        self.cfg = moe_product_config(max_rows, n, k, types[out_dtype])
-        self.out_dtype = out_dtype or torch.bfloat16
+        self._set_shape(moe_product_config(max_rows, n, k, types[out_dtype]),
+                        out_dtype or torch.bfloat16)
         self.handle, self.ws_bytes = moe_product_create(self.cfg)
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8,
                                      device=device if device is not None else "cuda")
+
+    def _set_shape(self, cfg: moe_product_config, out_dtype):
+        self.cfg, self.out_dtype = cfg, out_dtype
+        self._n, self._k, self._kb = cfg.n, cfg.k, _groups(cfg.k)
+        self._w_shape, self._ws_shape = (cfg.n, cfg.k), (_groups(cfg.n), _groups(cfg.k))
 
     def forward(self, a, a_scales, w, w_scales, out, stream=None):
         """out [rows, n] = (a scaled by a_scales) (w scaled by w_scales)^T: a e4m3 [rows, k],
         a_scales fp32 [rows, ceil(k/128)], w e4m3 [n, k], w_scales fp32 [ceil(n/128),
         ceil(k/128)].  Rows of out may be strided (a slice of a wider tensor)."""
-        n, k = self.cfg.n, self.cfg.k
         rows = a.shape[0]
-        want = {"a": (a, (rows, k)), "a_scales": (a_scales, (rows, _groups(k))), "w": (w, (n, k)),
-                "w_scales": (w_scales, (_groups(n), _groups(k))), "out": (out, (rows, n))}
-        for name, (t, shape) in want.items():
-            if tuple(t.shape) != shape:
+        for name, t, shape in (("a", a, (rows, self._k)), ("a_scales", a_scales, (rows, self._kb)),
+                               ("w", w, self._w_shape), ("w_scales", w_scales, self._ws_shape),
+                               ("out", out, (rows, self._n))):
+            if t.shape != shape:
                 raise ValueError(f"{name}: shape {tuple(t.shape)}, the product needs {shape}")
         if out.dtype != self.out_dtype:
             raise ValueError(f"out: element type {out.dtype}, the product needs {self.out_dtype}")
-        ldo = _rows_of(out, "out", _BF16 + _F32)[1]
-        _on_one_device(a=a, a_scales=a_scales, w=w, w_scales=w_scales, out=out,
-                       workspace=self.workspace)
-        moe_block_scaled_product(self.handle, a, a_scales, w, w_scales, rows, out, ldo,
+        _on_current_device((a, a_scales, w, w_scales, out, self.workspace))
+        addr, ldo = _rows_of(out, "out", _BF16 + _F32)
+        moe_block_scaled_product(self.handle, a, a_scales, w, w_scales, rows, addr, ldo,
                                  self.workspace, self.ws_bytes, stream)
 
     def device_status(self, stream=None) -> int:

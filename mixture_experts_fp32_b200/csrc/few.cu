@@ -41,13 +41,13 @@ template <bool FP8>
 struct FewSmem {
   static constexpr int kParts = FP8 ? 1 : 2;          // of h
   WsSmem<kParts * kTokens, kTokens, FP8 ? 6 : 5> ws;
-  float sums[kWsWorkers][kTokens];                    // router
   float w[kTokens][kMaxTopK];                         // routing weights
   int ids[kTokens][kMaxTopK];                         // routed experts, -1 in padding rows
   short active[kFewSlots];                            // the distinct experts, ascending
   signed char pick[kFewSlots + 1][kTokens];           // j with ids[t][j] = active[slot], or -1
   unsigned int bitmap[kMaxExperts / 32];
-  uint64_t routed, met;                               // selection made; h complete
+  // router's weights read; x quantised; selection made; h complete
+  uint64_t scored, ready, routed, met;
   int flag;
 };
 
@@ -60,16 +60,24 @@ __device__ __forceinline__ uint32_t two_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // The workers' and promoters' part.
 template <bool FP8>
 __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, int ch_h, int ch_i,
-                                            int ch_s, int units_s) {
+                                            int ch_s) {
   using S = decltype(s.ws);
   constexpr int EB = FP8 ? 1 : 2;
   constexpr int kParts = FewSmem<FP8>::kParts;
-  const int tid = (int)threadIdx.x - kWsFirst, lane = threadIdx.x & 31;
-  const int warp = (int)(threadIdx.x >> 5) - 4;       // workers 0 .. 7
-  const bool worker = warp >= 0 && warp < kWsWorkers, promoter = (warp & 3) == 0;
+  const int tid = ws_worker_thread(), warp = tid >> 5, lane = threadIdx.x & 31;
+  const bool worker = tid >= 0, promoter = !worker;
   const int cta = blockIdx.x, ctas = gridDim.x;
   const int kb_h = p.H / 128, kb_i = p.imax / 128;
   const WsRole role{p.wait_limit_ns, p.status, p.timeout_bit};
@@ -79,9 +87,7 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
   auto grid_sync = [&](unsigned int* counter) {
     ws_workers_sync();
     if (tid == 0) {
-      __threadfence();
-      atomicAdd(counter, 1u);
-      bool met = ld_acquire_gpu(counter) >= (unsigned int)ctas;
+      bool met = atomic_add_acq_rel(counter) + 1 >= (unsigned int)ctas;
       const uint64_t t0 = global_timer_ns();
       while (!met) {
         met = ld_acquire_gpu(counter) >= (unsigned int)ctas;
@@ -97,50 +103,69 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
   };
 
   if (worker) {
-    // ---- 1. router logits of all tokens, items (expert, K split)
-    for (int item = cta; item < p.E * p.router_splits; item += ctas) {
-      const int split = item / p.E, e = item - split * p.E;
-      const int k0 = split * p.router_k, k1 = min(p.H, k0 + p.router_k);
-      const float* wr = p.router_w + (size_t)e * p.H;
-      float acc[kTokens];
+    // ---- 1. router logits: eight experts and a part of K a CTA, on m16n8k16 products with the
+    // fp32 weights split exactly into three bf16 parts (each the nearest bf16 of what is
+    // left), so the sums are the fp32 sums with the full weights.  Few instructions, as for
+    // the selection below: every launch fetches this code anew.  (As an unrolled loop of
+    // fp32 FMAs, sixteen tokens took 32000 clocks.)
+    const int groups = (p.E + 7) / 8, chunks = p.H / 32;
+    if (cta < groups * p.router_splits) {
+      const int split = cta / groups, e0 = (cta - split * groups) * 8;
+      const int g = lane >> 2, q = lane & 3;
+      const int end = chunks * (split + 1) / p.router_splits;
+      const float* wr = p.router_w + (size_t)min(e0 + g, p.E - 1) * p.H + 8 * q;
+      const __nv_bfloat16* x0 = p.x + (size_t)g * p.H + 8 * q;
+      const __nv_bfloat16* x1 = x0 + (size_t)8 * p.H;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int c = chunks * split / p.router_splits + warp; c < end; c += 4 * kWsWorkers) {
+        float4 w[4][2];                               // the loads of four chunks go out together
+        uint4 a[4][2];
 #pragma unroll
-      for (int t = 0; t < kTokens; ++t) acc[t] = 0.f;
-      for (int k = k0 + warp * 256 + lane * 8; k < k1; k += kWsWorkers * 256) {
-        const float4 w0 = __ldg(reinterpret_cast<const float4*>(wr + k));
-        const float4 w1 = __ldg(reinterpret_cast<const float4*>(wr + k + 4));
-        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        for (int j = 0; j < 4; ++j) {
+          const int cj = c + j * kWsWorkers;
+          w[j][0] = w[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          a[j][0] = a[j][1] = make_uint4(0, 0, 0, 0);
+          if (cj < end) {
+            w[j][0] = __ldg(reinterpret_cast<const float4*>(wr + cj * 32));
+            w[j][1] = __ldg(reinterpret_cast<const float4*>(wr + cj * 32) + 1);
+            if (g < p.T) a[j][0] = __ldg(reinterpret_cast<const uint4*>(x0 + cj * 32));
+            if (g + 8 < p.T) a[j][1] = __ldg(reinterpret_cast<const uint4*>(x1 + cj * 32));
+          }
+        }
 #pragma unroll
-        for (int t0 = 0; t0 < kTokens; t0 += 4) {
-          if (t0 >= p.T) break;
-          uint4 xv[4];                                // rows past T repeat the last token
+        for (int j = 0; j < 4; ++j) {
+          float f[8] = {w[j][0].x, w[j][0].y, w[j][0].z, w[j][0].w,
+                        w[j][1].x, w[j][1].y, w[j][1].z, w[j][1].w};
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
-            xv[t] = __ldg(
-                reinterpret_cast<const uint4*>(p.x + (size_t)min(t0 + t, p.T - 1) * p.H + k));
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t r[4] = {xv[t].x, xv[t].y, xv[t].z, xv[t].w};
+          for (int part = 0; part < 3; ++part) {
+            uint32_t b[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              acc[t0 + t] = fmaf(__uint_as_float(r[i] << 16), w[2 * i], acc[t0 + t]);
-              acc[t0 + t] = fmaf(__uint_as_float(r[i] & 0xffff0000u), w[2 * i + 1], acc[t0 + t]);
+              b[i] = two_bf16(f[2 * i], f[2 * i + 1]);
+              f[2 * i] -= __uint_as_float(b[i] << 16);
+              f[2 * i + 1] -= __uint_as_float(b[i] & 0xffff0000u);
             }
+            mma_bf16(acc, a[j][0].x, a[j][1].x, a[j][0].y, a[j][1].y, b[0], b[1]);
+            mma_bf16(acc, a[j][0].z, a[j][1].z, a[j][0].w, a[j][1].w, b[2], b[3]);
           }
         }
       }
+      if (lane == 0) mbar_arrive(smem_u32(&s.scored));
+      // the warps' sums meet where tiles will lie later
+      auto* sums = reinterpret_cast<float(*)[kTokens][8]>(&s.ws.tile[0][0]);
 #pragma unroll
-      for (int t = 0; t < kTokens; ++t) {
+      for (int i = 0; i < 4; ++i) sums[warp][g + 8 * (i >> 1)][2 * q + (i & 1)] = acc[i];
+      ws_workers_sync();
+      const int t = tid >> 3, e = e0 + (tid & 7);
+      if (t < p.T && e < p.E) {
+        float l = split == 0 && p.router_b != nullptr ? p.router_b[e] : 0.f;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], off);
-        if (lane == 0) s.sums[warp][t] = acc[t];
+        for (int w = 0; w < kWsWorkers; ++w) l += sums[w][t][tid & 7];
+        p.logits[((size_t)split * kTokens + t) * p.E + e] = l;
       }
-      ws_workers_sync();
-      if (tid < p.T) {
-        float l = 0.f;
-        for (int w = 0; w < kWsWorkers; ++w) l += s.sums[w][tid];
-        p.logits[((size_t)split * kTokens + tid) * p.E + e] = l;
-      }
-      ws_workers_sync();
+    } else if (lane == 0) {
+      mbar_arrive(smem_u32(&s.scored));
     }
     // counters of phases 2 and 3
     if (tid < 3) p.split_count[tid * kFewMaxCtas + cta] = 0;
@@ -160,6 +185,7 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
     }
     if (FP8) fence_proxy_async();                       // the codes are read by TMA
     grid_sync(p.bar);
+    if (FP8 && tid == 0) mbar_arrive(smem_u32(&s.ready));
 
     // ---- 2a. the experts of every token, by every CTA for itself
     for (int t = warp; t < p.T; t += kWsWorkers) {
@@ -172,23 +198,28 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
       float v[8];
       uint32_t key[8];
 #pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll 1
+      for (int sp = 0; sp < p.router_splits; sp += 4) {
+        float part[4][8];                             // every load before the first use
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            part[j][i] = sp + j < p.router_splits && lane + 32 * i < p.E
+                             ? __ldcg(p.logits + ((size_t)(sp + j) * kTokens + t) * p.E + lane +
+                                      32 * i)
+                             : 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += part[j][i];
+      }
+#pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int e = lane + 32 * i;
-        float part[kFewRouterSplits], bias = 0.f;       // every load before the first use
-        if (e < p.E) {
-          if (p.router_b != nullptr) bias = p.router_b[e];
-#pragma unroll
-          for (int sp = 0; sp < kFewRouterSplits; ++sp)
-            if (sp < p.router_splits)
-              part[sp] = __ldcg(p.logits + ((size_t)sp * kTokens + t) * p.E + e);
-        }
-        v[i] = 0.f;
         key[i] = 0;
         if (e < p.E) {
-#pragma unroll
-          for (int sp = 0; sp < kFewRouterSplits; ++sp)
-            if (sp < p.router_splits) v[i] += part[sp];
-          v[i] += bias;
           const uint32_t u = __float_as_uint(v[i] + 0.f);
           key[i] = max(u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u), 1u);
           if (cta == 0 && p.logits_out != nullptr)
@@ -255,10 +286,6 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
     ws_workers_sync();
     if (tid == 0) mbar_arrive(smem_u32(&s.routed));
   }
-  ws_tile_free();                                     // the other promoters learn of the selection
-  int A = 0;
-#pragma unroll
-  for (int i = 0; i < kMaxExperts / 32; ++i) A += __popc(s.bitmap[i]);
 
   auto on = [&](int slot, int t) { return t < p.T && s.pick[slot][t] >= 0; };
   auto h_row = [&](int slot, int t) {                 // its high part; the low one kTokens below
@@ -269,9 +296,9 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
   const int t_lane = lane & (kTokens - 1);            // a promoter lane's token
 
   // ---- 2b. gate/up: columns 0 .. 127 of a tile are gate values, 128 .. 255 up values
-  auto gate_up = [&](bool routed, int I, int units, unsigned int* split_count, float* parts) {
+  auto gate_up = [&](bool routed, int I, int experts, unsigned int* split_count, float* parts) {
     const int ft = I / 128;
-    const WsSplit split(units, ctas);
+    const WsSplit split(experts * ft, ch_h, ctas);
     const int u1 = split.begin(cta + 1);
     for (int u = split.begin(cta); u < u1;) {
       const int tile = u / ch_h, c0 = u - tile * ch_h, c1 = min(ch_h, c0 + (u1 - u)), t0 = u - c0;
@@ -280,14 +307,9 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
       if (promoter) {
         sum.clear();
         if (FP8) {
-          const float* sw = routed ? p.s_gate_up + (size_t)s.active[slot] * (2 * I / 128) * kb_h
-                                   : p.ss_gate_up;
-          WsScales w, x;
-          w.reset(sw + (size_t)((f + (threadIdx.x < 256 ? 0 : I)) / 128) * kb_h, kb_h, c0);
-          x.reset(p.sx + (size_t)t_lane * kb_h, lane < p.T ? kb_h : 0, c0);
-          for (int c = c0; c < c1; ++c) sum.add(w.at(c) * x.at(c), lane < p.T);
+          for (int c = c0; c < c1; ++c) sum.template add<true>(1.f, lane < p.T);
         } else {
-          sum.add(1.f, lane < p.T);
+          sum.template add<false>(1.f, lane < p.T);
         }
       }
       ws_tile_free();
@@ -342,9 +364,18 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
       }
     }
   };
-  if (p.S) gate_up(false, p.Is, units_s, p.split_count, p.part);
-  gate_up(true, p.I, A * (p.I / 128) * ch_h, p.split_count + kFewMaxCtas,
-          p.part + (size_t)kFewMaxCtas * 2 * kTokens * kWsRows);
+  // the promoters are at the shared expert while the workers still select the routed ones
+  int A = 0;
+#pragma unroll 1                                      // one copy of the code
+  for (int routed = 0; routed < 2; ++routed) {
+    if (routed) {
+      ws_tile_free();                                 // now the selection is known to both
+#pragma unroll
+      for (int i = 0; i < kMaxExperts / 32; ++i) A += __popc(s.bitmap[i]);
+    }
+    gate_up(routed, routed ? p.I : p.Is, routed ? A : p.S, p.split_count + routed * kFewMaxCtas,
+            p.part + (size_t)routed * kFewMaxCtas * 2 * kTokens * kWsRows);
+  }
   if (worker) {
     fence_proxy_async();                              // h is read by TMA
     grid_sync(p.bar + 1);
@@ -359,17 +390,14 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
       reinterpret_cast<uint4*>(p.out)[i] = make_uint4(0, 0, 0, 0);
     return;
   }
-  if (FP8 && promoter) sum.role.wait(&s.met, 0);      // scales of h
   const int per = ch_s + A * ch_i;
-  const WsSplit split((p.H + kWsRows - 1) / kWsRows * per, ctas);
+  const WsSplit split((p.H + kWsRows - 1) / kWsRows, per, ctas);
   const int u1 = split.begin(cta + 1);
   for (int u = split.begin(cta); u < u1;) {
     const int tile = u / per, c0 = u - tile * per, c1 = min(per, c0 + (u1 - u)), t0 = u - c0;
     u += c1 - c0;
     if (promoter) {
       sum.clear();
-      // its columns' row of scale blocks; past the end of H the last one, whose sums are not used
-      const int rb = min(tile * 2 + (threadIdx.x < 256 ? 0 : 1), kb_h - 1);
       for (int c = c0; c < c1;) {
         // the run of stages of one slot
         const int slot = c < ch_s ? kShared : (c - ch_s) / ch_i;
@@ -379,15 +407,9 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
         const bool take = (!FP8 || lane < kTokens) && on(slot, t_lane);
         const float f = take && slot != kShared ? s.w[t_lane][(int)s.pick[slot][t_lane]] : 1.f;
         if (FP8) {
-          const int kbs = (slot == kShared ? p.Is : p.I) / 128;
-          WsScales w, x;
-          w.reset(slot == kShared ? p.ss_down + (size_t)rb * kbs
-                                  : p.s_down + ((size_t)s.active[slot] * kb_h + rb) * kbs,
-                  kbs, c - first);
-          x.reset(p.sh + h_row(slot, t_lane) * kb_i, take ? kbs : 0, c - first);
-          for (; c < end; ++c) sum.add(f * (w.at(c - first) * x.at(c - first)), take);
+          for (; c < end; ++c) sum.template add<true>(f, take);
         } else {
-          sum.add(f, take);
+          sum.template add<false>(f, take);
           c = end;
         }
       }
@@ -424,18 +446,6 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
   }
 }
 
-// f(tile, c, first, last) for every unit of this CTA's share: stage c of a tile of `per`
-// stages, whether it begins or ends this CTA's run of the tile.
-template <class F>
-__device__ __forceinline__ void each_unit(int units, int per, F&& f) {
-  const WsSplit split(units, gridDim.x);
-  const int u0 = split.begin(blockIdx.x), u1 = split.begin(blockIdx.x + 1);
-  for (int u = u0; u < u1; ++u) {
-    const int tile = u / per, c = u - tile * per;
-    f(tile, c, u == u0 || c == 0, u + 1 == u1 || c + 1 == per);
-  }
-}
-
 template <bool FP8>
 __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant__ FewMaps maps,
                                                           const FewArgs p) {
@@ -448,10 +458,12 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
   const int ch_h = p.H * EB / kWsBytes;               // stages of a gate/up tile
   const int ch_i = p.I * EB / kWsBytes;               // stages of a slot of a down tile
   const int ch_s = p.S ? p.Is * EB / kWsBytes : 0;
-  const int units_s = p.S ? p.Is / 128 * ch_h : 0;
+  const int tiles_s = p.S * (p.Is / 128);
   const int down_tiles = (p.H + kWsRows - 1) / kWsRows;
 
   if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&s.scored), kWsWorkers);
+    mbar_init(smem_u32(&s.ready), 1);
     mbar_init(smem_u32(&s.routed), 1);
     mbar_init(smem_u32(&s.met), 1);
   }
@@ -480,21 +492,23 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
   if (warp == 1) {
     // ------------------------------------------------------------- weight producer
     WsWeights<S> out(s.ws, role);
-    auto gate_up = [&](const CUtensorMap* m, int I, int units, bool routed) {
+    auto gate_up = [&](const CUtensorMap* m, int I, int tiles, bool routed) {
       const int ft = I / 128;
-      each_unit(units, ch_h, [&](int tile, int c, bool, bool) {
+      ws_each_unit(tiles, ch_h, [&](int tile, int c, bool, bool) {
         const int slot = routed ? tile / ft : 0, f = (routed ? tile - slot * ft : tile) * 128;
         const int row = (routed ? s.active[slot] * 2 * I : 0) + f;
         out.load(m, row, row + I, c * kWsBytes);
       });
     };
-    gate_up(&maps.shared_gate_up, p.Is, units_s, false);
+    // the router's few loads first: behind a ring's worth of weights they would wait 4 us
+    out.role.wait(&s.scored, 0);
+    gate_up(&maps.shared_gate_up, p.Is, tiles_s, false);
     if (out.role.wait(&s.routed, 0)) {
       const int A = count_active();
-      gate_up(&maps.gate_up, p.I, A * (p.I / 128) * ch_h, true);
+      gate_up(&maps.gate_up, p.I, A * (p.I / 128), true);
       if (A > 0) {
         const int per = ch_s + A * ch_i;
-        each_unit(down_tiles * per, per, [&](int tile, int c, bool, bool) {
+        ws_each_unit(down_tiles, per, [&](int tile, int c, bool, bool) {
           int ci;
           const int slot = down_slot(c, &ci), r = tile * kWsRows;
           const int row = (slot == kShared ? 0 : s.active[slot] * p.H) + r;
@@ -507,18 +521,18 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
   } else if (warp == 2) {
     // ------------------------------------------------------------------ MMA issuer
     WsMma<FP8, S> mma(s.ws, role);
-    auto gate_up = [&](int units) {
-      each_unit(units, ch_h, [&](int, int, bool first, bool last) {
+    auto gate_up = [&](int tiles) {
+      ws_each_unit(tiles, ch_h, [&](int, int, bool first, bool last) {
         mma.stage(FP8 || first, FP8 || last);
       });
     };
-    gate_up(units_s);
+    gate_up(tiles_s);
     if (mma.role.wait(&s.routed, 0)) {
       const int A = count_active();
-      gate_up(A * (p.I / 128) * ch_h);
+      gate_up(A * (p.I / 128));
       if (A > 0) {
         const int per = ch_s + A * ch_i;
-        each_unit(down_tiles * per, per, [&](int, int c, bool first, bool last) {
+        ws_each_unit(down_tiles, per, [&](int, int c, bool first, bool last) {
           int ci;
           const bool shared = down_slot(c, &ci) == kShared;
           mma.stage(FP8 || first || ci == 0, FP8 || last || ci + 1 == (shared ? ch_s : ch_i));
@@ -529,30 +543,62 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
   } else if (warp == 3) {
     // --------------------------------------------------------- activation producer
     WsActivations<S> out(s.ws, role);
-    auto gate_up = [&](int units) {
-      each_unit(units, ch_h, [&](int, int c, bool, bool) {
-        out.load(&maps.x, 0, c * kWsBytes, kTokens);
-      });
+    const int lane = threadIdx.x & 31, kb_h = p.H / 128;
+    auto gate_up = [&](int I, int experts, bool routed) {
+      const int ft = I / 128;
+      ws_each_unit_ahead(
+          experts * ft, ch_h,
+          [&](int tile, int c) {
+            WsScale sc;
+            if (FP8) {
+              const int slot = routed ? tile / ft : 0, f = routed ? tile - slot * ft : tile;
+              const float* sw = routed ? p.s_gate_up + (size_t)s.active[slot] * 2 * ft * kb_h
+                                       : p.ss_gate_up;
+              if (lane < p.T) sc.x = __ldcg(p.sx + (size_t)lane * kb_h + c);
+              if (lane < 2) sc.w = __ldg(sw + (size_t)(f + lane * ft) * kb_h + c);
+            }
+            return sc;
+          },
+          [&](int, int c, const WsScale& sc) {
+            out.template load<FP8>(&maps.x, 0, c * kWsBytes, kTokens, sc);
+          });
     };
-    if (!FP8) gate_up(units_s);                       // FP8: x is quantised before the selection
+    if (FP8 && out.role.wait(&s.ready, 0)) fence_proxy_async();
+    gate_up(p.Is, p.S, false);
     if (out.role.wait(&s.routed, 0)) {
-      fence_proxy_async();
       const int A = count_active();
-      if (FP8) gate_up(units_s);
-      gate_up(A * (p.I / 128) * ch_h);
+      gate_up(p.I, A, true);
       if (A > 0 && out.role.wait(&s.met, 0)) {
         fence_proxy_async();
-        const int per = ch_s + A * ch_i;
-        each_unit(down_tiles * per, per, [&](int, int c, bool, bool) {
-          int ci;
-          const int slot = down_slot(c, &ci);
-          out.load(&maps.h, (slot == kShared ? 0 : slot + p.S) * S::ROWS, ci * kWsBytes, S::ROWS);
-        });
+        const int per = ch_s + A * ch_i, kb_i = p.imax / 128;
+        ws_each_unit_ahead(
+            down_tiles, per,
+            [&](int tile, int c) {
+              WsScale sc;
+              if (FP8) {
+                int ci;
+                const int slot = down_slot(c, &ci), kbs = (slot == kShared ? p.Is : p.I) / 128;
+                const int row = (slot == kShared ? 0 : slot + p.S) * kTokens + lane;
+                const float* sw = slot == kShared
+                                      ? p.ss_down
+                                      : p.s_down + (size_t)s.active[slot] * kb_h * kbs;
+                if (lane < p.T) sc.x = __ldcg(p.sh + (size_t)row * kb_i + ci);
+                // past the end of H the last block, whose sums are not used
+                if (lane < 2) sc.w = __ldg(sw + (size_t)min(2 * tile + lane, kb_h - 1) * kbs + ci);
+              }
+              return sc;
+            },
+            [&](int, int c, const WsScale& sc) {
+              int ci;
+              const int slot = down_slot(c, &ci);
+              out.template load<FP8>(&maps.h, (slot == kShared ? 0 : slot + p.S) * S::ROWS,
+                                     ci * kWsBytes, S::ROWS, sc);
+            });
       }
     }
     out.drain();
   } else {
-    few_compute<FP8>(s, p, ch_h, ch_i, ch_s, units_s);
+    few_compute<FP8>(s, p, ch_h, ch_i, ch_s);
   }
   ws_teardown(s.ws);
 }
@@ -609,11 +655,11 @@ cudaError_t prepare_few_kernels() {
 
 cudaError_t launch_few(FewArgs a, bool fp8, int num_sms, cudaStream_t st) {
   const int ctas = num_sms < kFewMaxCtas ? num_sms : kFewMaxCtas;
-  // with fewer experts than CTAs the dot products are cut along K too
-  int splits = ctas / a.E;
-  splits = splits < 1 ? 1 : splits > kFewRouterSplits ? kFewRouterSplits : splits;
-  a.router_k = ((a.H + splits - 1) / splits + 255) / 256 * 256;
-  a.router_splits = (a.H + a.router_k - 1) / a.router_k;
+  // eight experts a CTA; with CTAs left over K is cut too, a chunk of 32 a warp at least
+  const int groups = (a.E + 7) / 8;
+  const int most = a.H / 32 / kWsWorkers < kFewRouterSplits ? a.H / 32 / kWsWorkers : kFewRouterSplits;
+  a.router_splits = ctas / groups < most ? ctas / groups : most;
+  if (a.router_splits < 1) a.router_splits = 1;
   const uint64_t eb = fp8 ? 1 : 2, E = a.E, H = a.H, I = a.I, Is = a.Is;
   FewMaps m;
   if (!ws_map(&m.gate_up, a.w_gate_up, H * eb, E * 2 * I, kWsBoxRows) ||

@@ -160,7 +160,7 @@ cudaError_t prepare_grouped_gemm_kernels();
 // The few-token layer (few.cu).
 constexpr int kFewSlots = MOE_FEW_TOKENS_MAX * kMaxTopK;   // distinct experts, at most
 constexpr int kFewMaxCtas = 160;
-constexpr int kFewRouterSplits = 4;
+constexpr int kFewRouterSplits = 16;
 struct FewArgs {
   const __nv_bfloat16* x;
   const uint8_t* valid;
@@ -171,7 +171,7 @@ struct FewArgs {
   __nv_bfloat16* out;
   // workspace
   float* logits;                 // [router splits][MOE_FEW_TOKENS_MAX][E]
-  int router_splits, router_k;   // K splits of the router, values of K in each
+  int router_splits;             // K splits of the router
   int h_slots;                   // expert slots of h (shared expert first)
   uint8_t* h;                    // [slot][token][imax] codes; bf16: [slot][high, low][token][imax]
   float* sh;                     // FP8: scales of h

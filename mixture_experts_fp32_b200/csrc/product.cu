@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kWsBlock, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
   const int per = p.kb;                               // stages of a tile
-  const WsSplit split((p.N + kWsRows - 1) / kWsRows * per, ctas);
+  const WsSplit split((p.N + kWsRows - 1) / kWsRows, per, ctas);
   const int ub = split.begin(cta), ue = split.begin(cta + 1);
   const WsRole role{p.wait_limit_ns, p.status, MOE_DEV_WAIT_TIMEOUT_PRODUCT};
   ws_setup(s.ws);
@@ -100,23 +100,29 @@ __global__ void __launch_bounds__(kWsBlock, 1)
     mma.drain();
   } else if (warp == 3) {
     WsActivations<S> out(s.ws, role);
-    for (int u = ub; u < ue; ++u) out.load(&amap, 0, u % per * kWsBytes, ROWS);
+    ws_each_unit_ahead(
+        (p.N + kWsRows - 1) / kWsRows, per,
+        [&](int tile, int c) {
+          WsScale sc;
+          if (lane < p.M) sc.x = __ldg(p.sa + (size_t)lane * p.kb + c);
+          // past the end of N the last block, whose sums are not used
+          if (lane < 2) sc.w = __ldg(p.sw + (size_t)min(2 * tile + lane, (p.N - 1) / 128) * p.kb + c);
+          return sc;
+        },
+        [&](int, int c, const WsScale& sc) {
+          out.template load<true>(&amap, 0, c * kWsBytes, ROWS, sc);
+        });
     out.drain();
   } else {
-    const bool worker = ws_is_worker(warp), promoter = (warp & 3) == 0;
-    const int tid = (int)threadIdx.x - kWsFirst;
+    const int tid = ws_worker_thread();
+    const bool worker = tid >= 0, promoter = !worker;
     WsPromoter<S> sum(s.ws, role);
     for (int u = ub; u < ue;) {
       const int tile = u / per, c0 = u - tile * per, c1 = min(per, c0 + (ue - u)), t0 = u - c0;
       u += c1 - c0;
       if (promoter) {
         sum.clear();
-        // its columns' row of scale blocks; past the end of N the last one, whose sums are not used
-        const int rb = min(tile * 2 + (threadIdx.x < 256 ? 0 : 1), (p.N - 1) / 128);
-        WsScales w, x;
-        w.reset(p.sw + (size_t)rb * p.kb, p.kb, c0);
-        x.reset(p.sa + (size_t)lane * p.kb, lane < p.M ? p.kb : 0, c0);
-        for (int c = c0; c < c1; ++c) sum.add(w.at(c) * x.at(c), lane < p.M);
+        for (int c = c0; c < c1; ++c) sum.template add<true>(1.f, lane < p.M);
       }
       ws_tile_free();
       if (promoter) sum.park(ROWS);

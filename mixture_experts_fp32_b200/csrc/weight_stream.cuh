@@ -26,9 +26,10 @@
 // several CTAs is finished by the last of them to arrive, which adds the partial tiles
 // from global memory in CTA order, so results do not depend on timing.
 //
-// Thirteen warps: 1 weight producer, 2 MMA issuer, 3 activation producer; promoters 0, 4, 8,
-// 12 (lane: activation row; warp / 4: columns, i.e. weight rows, 64 (warp / 4) .. + 63);
-// workers 4 .. 11, who take a finished tile from shared memory.
+// Fifteen warps: 1 weight producer, 2 MMA issuer, 3 activation producer; promoters 0, 4, 8, 12
+// (lane: activation row; warp / 4: columns, i.e. weight rows, 64 (warp / 4) .. + 63); the
+// other eight are workers, who take a finished tile from shared memory while the promoters
+// are at the next one.
 #pragma once
 
 #include "moe_internal.cuh"
@@ -41,20 +42,26 @@ constexpr int kWsBoxRows = 128;               // rows of a TMA box of weights
 constexpr int kWsStageBytes = kWsRows * kWsBytes;
 constexpr int kWsWorkers = 8;                 // warps
 constexpr int kWsThreads = kWsWorkers * 32;   // worker threads
-constexpr int kWsFirst = 128;                 // first worker thread
-constexpr int kWsBlock = 13 * 32;
+constexpr int kWsBlock = 15 * 32;
 constexpr int kWsCols = kWsRows / 4;          // columns of a promoter
 constexpr int kWsTilePitch = kWsRows + 4;     // a finished tile in shared memory: rows apart
 constexpr unsigned long long kWsDrainNs = 1000000000ull;
+// FP8: scales of a stage (of its activation rows, and of its two blocks of 128 weight rows)
+// lie in a ring of slots.  No barrier guards a slot: the activation producer reaches stage
+// u + kWsSlots only after the MMAs of stage u + kWsSlots - STAGES, which waited for the
+// promoters to read the buffer two stages before that.
+constexpr int kWsSlots = 16;
 
 // Shared memory of the stream.  ROWS: activation rows brought (16 or 32), TILE: rows of a
 // finished tile.
 template <int ROWS_, int TILE, int STAGES_>
 struct WsSmem {
   static constexpr int ROWS = ROWS_, STAGES = STAGES_;
+  static_assert(STAGES + 2 < kWsSlots, "slots of scales");
   alignas(1024) uint8_t x[STAGES][ROWS * kWsBytes];   // MMAs read 128 rows from here: into w
   alignas(1024) uint8_t w[STAGES][kWsStageBytes];
   alignas(16) float tile[TILE][kWsTilePitch];
+  float scale[kWsSlots][ROWS + 2];
   uint64_t full_w[STAGES], full_x[STAGES], empty[STAGES], dfull[2], dempty[2], teardown;
   uint32_t tmem;
 };
@@ -65,13 +72,27 @@ bool ws_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64_t rows, in
 
 #if defined(__CUDACC__)
 
-// The even split of `units` over `ctas`: the first `more` CTAs take one unit more than `each`.
-// With fewer units than CTAs the CTAs behind the last unit have none.
+// The split of `tiles` tiles of `per` units over the CTAs: contiguous ranges, the first `more`
+// CTAs one unit more than `each`, the CTAs behind the last unit none.  Even over all CTAs,
+// unless that leaves one fewer than kWsLeast units: a shared tile costs its CTAs about what
+// four units take, so small work goes to fewer CTAs, whole tiles where these are short.
+constexpr int kWsLeast = 3;
 struct WsSplit {
   int each, more;
-  __device__ __forceinline__ WsSplit(int units, int ctas)
-      : each(units / ctas), more(units - units / ctas * ctas) {}
-  __device__ __forceinline__ int begin(int cta) const { return cta * each + min(cta, more); }
+  __device__ __forceinline__ WsSplit(int tiles, int per, int ctas) {
+    const int units = tiles * per;
+    if (units < ctas * kWsLeast)
+      ctas = tiles < ctas && per <= 2 * kWsLeast ? tiles
+                                                 : max(1, min(ctas, units / kWsLeast));
+    each = ctas > 0 ? units / ctas : 0;
+    more = units - each * ctas;
+    last = ctas;
+  }
+  int last;                                   // CTAs that take part
+  __device__ __forceinline__ int begin(int cta) const {
+    const int b = min(cta, last);
+    return b * each + min(b, more);
+  }
   __device__ __forceinline__ int owner(int u) const {
     const int head = more * (each + 1);
     return u < head ? u / (each + 1) : more + (u - head) / each;
@@ -193,18 +214,32 @@ struct WsWeights {
   }
 };
 
-// Activation producer (one warp): the same 128 bytes of K of activation rows row .. + ROWS - 1.
+// Activation producer (one warp): the same 128 bytes of K of activation rows row .. + ROWS - 1,
+// FP8 with the stage's scales: x of row `lane`, w of weight block `lane` (0, 1).
+struct WsScale {
+  float x = 0.f, w = 0.f;
+};
 template <class S>
 struct WsActivations {
   S& s;
   WsRole role;
   WsPos pos;
+  int slot = 0;
   uint64_t policy = policy_evict_last();      // and read again by every CTA
   uint32_t issued = 0, parity = 0;
   __device__ WsActivations(S& s_, const WsRole& r) : s(s_), role(r) {}
-  __device__ __forceinline__ void load(const CUtensorMap* m, int row, int koff, int box_rows) {
+  template <bool FP8>
+  __device__ __forceinline__ void load(const CUtensorMap* m, int row, int koff, int box_rows,
+                                       const WsScale& sc) {
     if (!role.wait(&s.empty[pos.i], pos.phase ^ 1u)) return;
-    if ((threadIdx.x & 31) == 0) {
+    const int lane = threadIdx.x & 31;
+    if (FP8) {
+      if (lane < S::ROWS) s.scale[slot][lane] = sc.x;
+      if (lane < 2) s.scale[slot][S::ROWS + lane] = sc.w;
+      slot = (slot + 1) % kWsSlots;
+      __syncwarp();
+    }
+    if (lane == 0) {
       const uint32_t bar = smem_u32(&s.full_x[pos.i]);
       mbar_arrive_expect_tx(bar, box_rows * kWsBytes);
       tma_load_2d(smem_u32(s.x[pos.i]), m, koff, row, bar, policy);
@@ -219,6 +254,40 @@ struct WsActivations {
         ws_wait(smem_u32(&s.full_x[i]), (parity >> i) & 1u, kWsDrainNs, role.status, role.bit);
   }
 };
+
+// f(tile, c, first, last) for every unit of this CTA's share: stage c of a tile of `per`
+// stages, whether it begins or ends this CTA's run of the tile.
+template <class F>
+__device__ __forceinline__ void ws_each_unit(int tiles, int per, F&& f) {
+  const WsSplit split(tiles, per, gridDim.x);
+  const int u0 = split.begin(blockIdx.x), u1 = split.begin(blockIdx.x + 1);
+  for (int u = u0; u < u1; ++u) {
+    const int tile = u / per, c = u - tile * per;
+    f(tile, c, u == u0 || c == 0, u + 1 == u1 || c + 1 == per);
+  }
+}
+// The same with what `fetch(tile, c)` gives for a unit, asked for four to eight units ahead (a
+// load takes up to two units' time behind a ring's worth of weights).
+template <class G, class F>
+__device__ __forceinline__ void ws_each_unit_ahead(int tiles, int per, G&& fetch, F&& f) {
+  const WsSplit split(tiles, per, gridDim.x);
+  const int u0 = split.begin(blockIdx.x), u1 = split.begin(blockIdx.x + 1);
+  WsScale cur[4], next[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (u0 + j < u1) cur[j] = fetch((u0 + j) / per, (u0 + j) % per);
+#pragma unroll 1
+  for (int u = u0; u < u1; u += 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (u + 4 + j < u1) next[j] = fetch((u + 4 + j) / per, (u + 4 + j) % per);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (u + j < u1) f((u + j) / per, (u + j) % per, cur[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cur[j] = next[j];
+  }
+}
 
 // MMA issuer (one warp in step, one lane issues): stages from `begin` to `end` share a buffer.
 template <bool FP8, class S>
@@ -268,18 +337,22 @@ struct WsPromoter {
   S& s;
   WsRole role;
   WsPos d;
+  int slot = 0;
   float acc[kWsCols];
   __device__ WsPromoter(S& s_, const WsRole& r) : s(s_), role(r) {}
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < kWsCols; ++i) acc[i] = 0.f;
   }
-  // acc += f * the next buffer, in lanes that `take` it; the buffer goes back as soon as it
-  // has been read
+  // acc += f * the next buffer (FP8: with the stage's scales), in lanes that `take` it; the
+  // buffer goes back as soon as it has been read
+  template <bool FP8>
   __device__ __forceinline__ void add(float f, bool take) {
     if (role.wait(&s.dfull[d.i], d.phase)) {
       tc_fence_after();
       const uint32_t at = s.tmem + d.i * kWsRows + (threadIdx.x >> 7) * kWsCols;
+      if (FP8)
+        f *= s.scale[slot][threadIdx.x & (S::ROWS - 1)] * s.scale[slot][S::ROWS + (threadIdx.x >> 8)];
 #pragma unroll
       for (int c = 0; c < kWsCols; c += 32) {
         float v[32];
@@ -296,6 +369,7 @@ struct WsPromoter {
       }
     }
     d.next(2);
+    if (FP8) slot = (slot + 1) % kWsSlots;
   }
   // the finished sums into the shared tile, rows 0 .. rows - 1
   __device__ __forceinline__ void park(int rows) {
@@ -309,54 +383,35 @@ struct WsPromoter {
   }
 };
 
-// Scales of consecutive K blocks from a row of them (a row a lane, or one for all): four in
-// use, four under way.
-struct WsScales {
-  const float* row = nullptr;
-  int n = 0, base = 0;
-  float cur[4], nxt[4];
-  __device__ __forceinline__ void fetch(int kb, float (&o)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = kb + i < n ? __ldcg(row + kb + i) : 0.f;
-  }
-  // scales of blocks kb, kb + 1, ..; n = 0: none
-  __device__ __forceinline__ void reset(const float* r, int blocks, int kb) {
-    row = r;
-    n = blocks;
-    base = kb;
-    fetch(kb, cur);
-    fetch(kb + 4, nxt);
-  }
-  // that of block kb, which grows by one from call to call
-  __device__ __forceinline__ float at(int kb) {
-    if (kb == base + 4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
-      base = kb;
-      fetch(kb + 4, nxt);
-    }
-    const int i = kb - base;
-    return i == 0 ? cur[0] : i == 1 ? cur[1] : i == 2 ? cur[2] : cur[3];
-  }
-};
-
-__device__ __forceinline__ bool ws_is_worker(int warp) { return warp >= 4 && warp < 12; }
+// A worker's thread index 0 .. kWsThreads - 1, or -1.
+__device__ __forceinline__ int ws_worker_thread() {
+  const int warp = threadIdx.x >> 5;
+  if (warp < 5 || (warp & 3) == 0) return -1;
+  return (warp - 5 - (warp > 8) - (warp > 12)) * 32 + (int)(threadIdx.x & 31);
+}
+__device__ __forceinline__ bool ws_is_promoter() { return ((threadIdx.x >> 5) & 3) == 0; }
 __device__ __forceinline__ void ws_workers_sync() { named_bar_sync(1, kWsThreads); }
 // promoters and workers: the shared tile may be written / has been written
-__device__ __forceinline__ void ws_tile_free() { named_bar_sync(2, kWsThreads + 64); }
-__device__ __forceinline__ void ws_tile_ready() { named_bar_sync(3, kWsThreads + 64); }
+__device__ __forceinline__ void ws_tile_free() { named_bar_sync(2, kWsThreads + 128); }
+__device__ __forceinline__ void ws_tile_ready() { named_bar_sync(3, kWsThreads + 128); }
+
+// One more on a counter of the device: what this CTA's threads stored before (and a barrier
+// ordered before this) is visible to who adds after, and the other way round.
+__device__ __forceinline__ unsigned int atomic_add_acq_rel(unsigned int* p) {
+  unsigned int v;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 
 // Several CTAs share something: true, for all workers, in the CTA that arrives last.  What the
 // others' workers stored before is visible after.
 __device__ __forceinline__ bool ws_arrive_last(unsigned int* counter, unsigned int expected,
                                                int* flag, bool reset) {
   ws_workers_sync();
-  if (threadIdx.x == kWsFirst) {
-    __threadfence();
-    const bool last = atomicAdd(counter, 1u) + 1 == expected;
+  if (ws_worker_thread() == 0) {
+    const bool last = atomic_add_acq_rel(counter) + 1 == expected;
     if (last && reset) *counter = 0;
     *flag = last;
-    __threadfence();
   }
   ws_workers_sync();
   return *flag != 0;
@@ -403,7 +458,7 @@ template <int ROWS>
 __device__ __forceinline__ void ws_store_partial(const float (*tile)[kWsTilePitch], float* part,
                                                  int cta, int b0, int rows) {
   float* o = ws_partial<ROWS>(part, cta, b0);
-  for (int i = threadIdx.x - kWsFirst; i < rows * (kWsRows / 4); i += kWsThreads) {
+  for (int i = ws_worker_thread(); i < rows * (kWsRows / 4); i += kWsThreads) {
     const int row = i / (kWsRows / 4), c = i % (kWsRows / 4);
     reinterpret_cast<float4*>(o + row * kWsRows)[c] =
         reinterpret_cast<const float4*>(tile[row])[c];

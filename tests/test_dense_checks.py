@@ -156,9 +156,14 @@ def test_binding_refuses_bad_tensors():
 
 
 def test_product_binding_shapes():
-    p = moe.Product.__new__(moe.Product)
-    p.handle = None
-    p.cfg, p.out_dtype = moe.moe_product_config(8, 300, 144, moe.MOE_T_BF16), BF16
+    class HostOnly(moe.Product):
+        """The checks of ``forward`` without a workspace."""
+
+        def __init__(self):
+            self.handle = None
+            self._set_shape(moe.moe_product_config(8, 300, 144, moe.MOE_T_BF16), BF16)
+
+    p = HostOnly()
     good = dict(a=Fake((5, 144), F8), a_scales=Fake((5, 2), F32), w=Fake((300, 144), F8),
                 w_scales=Fake((3, 2), F32), out=Fake((5, 300)))
     for name, bad in (("a", Fake((5, 128), F8)), ("a_scales", Fake((5, 1), F32)),
