@@ -731,8 +731,8 @@ class Product:
                 raise ValueError(f"{name}: shape {tuple(t.shape)}, the product needs {shape}")
         if out.dtype != self.out_dtype:
             raise ValueError(f"out: element type {out.dtype}, the product needs {self.out_dtype}")
-        _on_current_device((a, a_scales, w, w_scales, out, self.workspace))
         addr, ldo = _rows_of(out, "out", _BF16 + _F32)
+        _on_current_device((a, a_scales, w, w_scales, out, self.workspace))
         moe_block_scaled_product(self.handle, a, a_scales, w, w_scales, rows, addr, ldo,
                                  self.workspace, self.ws_bytes, stream)
 

@@ -10,8 +10,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_b200.so")
 SOURCES = ["moe_api.cu", "router_tc.cu", "topk.cu", "routing.cu", "grouped_gemm.cu",
-           "grouped_gemm_fp8.cu", "noalloc.cu", "few.cu", "quantize.cu", "product.cu"]
-HEADERS = ["moe_internal.cuh", "weight_stream.cuh"]
+           "grouped_gemm_fp8.cu", "noalloc.cu", "few.cu", "quantize.cu", "product.cu",
+           "product_tiles.cu"]
+HEADERS = ["moe_internal.cuh", "weight_stream.cuh", "product.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

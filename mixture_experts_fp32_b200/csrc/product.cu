@@ -2,12 +2,13 @@
 //
 //   out[m, n] = sum_kb sa[m, kb] * sw[n / 128, kb] * sum_{k in kb} a[m, k] * w[n, k]
 //
-// Up to 32 rows: the weights stream once past all of them (weight_stream.cuh); HBM is the bound.
+// Here the entry points and the kernel of up to 32 rows: the weights stream once past all of them
+// (weight_stream.cuh); HBM is the bound.  More rows: product_tiles.cu.
 #include <string.h>
 
 #include <new>
 
-#include "weight_stream.cuh"
+#include "product.cuh"
 
 #define MOE_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -19,23 +20,6 @@ struct moe_product_s {
 
 namespace moe {
 namespace {
-
-constexpr int kMaxCtas = 160;
-
-struct ProductArgs {
-  const uint8_t* a;
-  const float* sa;
-  const uint8_t* w;
-  const float* sw;
-  void* out;
-  long long ldo;
-  int M, N, K, kb;
-  bool f32;
-  float* part;
-  unsigned int* counters;
-  unsigned int* status;
-  unsigned long long wait_limit_ns;
-};
 
 // out[m][n .. n + 3], n a multiple of 4, as far as n < N; one store where it is aligned.
 __device__ __forceinline__ void store_out4(const ProductArgs& p, int m, int n, const float (&v)[4]) {
@@ -149,10 +133,11 @@ __global__ void __launch_bounds__(kWsBlock, 1)
 }
 
 template <int ROWS>
-cudaError_t launch_rows(const CUtensorMap& w, const ProductArgs& a, int ctas, cudaStream_t st) {
-  CUtensorMap am;
-  if (!ws_map(&am, a.a, a.K, a.M, ROWS)) return cudaErrorInvalidValue;
-  product_rows_kernel<ROWS><<<ctas, kWsBlock, sizeof(RowsSmem<ROWS>) + 1024, st>>>(w, am, a);
+cudaError_t launch_rows(const ProductArgs& a, int ctas, cudaStream_t st) {
+  CUtensorMap am, wm;
+  if (!ws_map(&am, a.a, a.K, a.M, ROWS) || !ws_map(&wm, a.w, a.K, a.N, kWsBoxRows))
+    return cudaErrorInvalidValue;
+  product_rows_kernel<ROWS><<<ctas, kWsBlock, sizeof(RowsSmem<ROWS>) + 1024, st>>>(wm, am, a);
   return cudaGetLastError();
 }
 
@@ -167,8 +152,9 @@ cudaError_t prepare_rows() {
 }  // namespace
 
 cudaError_t prepare_product_kernels() {
-  const cudaError_t e = prepare_rows<16>();
-  return e == cudaSuccess ? prepare_rows<32>() : e;
+  cudaError_t e = prepare_rows<16>();
+  if (e == cudaSuccess) e = prepare_rows<32>();
+  return e == cudaSuccess ? prepare_product_tiles() : e;
 }
 
 }  // namespace moe
@@ -187,8 +173,12 @@ MOE_EXPORT moe_status moe_product_create(const moe_product_config* cfg, moe_prod
   p->cfg = *cfg;
   p->off_counters = 256;
   p->off_part = 256 + 1024;
-  p->ws_bytes = p->off_part + sizeof(float) * 2 * moe::kMaxCtas * moe::kWsRows *
-                                  (size_t)(cfg->max_rows <= 16 ? 16 : 32);
+  static_assert(sizeof(unsigned int) * moe::kProductCounters <= 1024, "");
+  // partial tiles: two a CTA of the weight stream, one a cluster pair of the tiles
+  const size_t stream = sizeof(float) * 2 * moe::kProductCtas * moe::kWsRows *
+                        (size_t)(cfg->max_rows <= 16 ? 16 : moe::kProductRows);
+  const size_t tiles = sizeof(float) * moe::kProductPairs * 256 * 256;
+  p->ws_bytes = p->off_part + (cfg->max_rows > moe::kProductRows && tiles > stream ? tiles : stream);
   p->wait_limit_ns = 2000000000ull;
   *product = p;
   *workspace_bytes = p->ws_bytes;
@@ -238,19 +228,14 @@ MOE_EXPORT moe_status moe_block_scaled_product(moe_product_t p, const void* a,
   g.counters = reinterpret_cast<unsigned int*>(ws + p->off_counters);
   g.status = reinterpret_cast<unsigned int*>(ws);
   g.wait_limit_ns = p->wait_limit_ns;
-  const int ctas = sms < moe::kMaxCtas ? sms : moe::kMaxCtas;
-  CUtensorMap wm;
-  if (!moe::ws_map(&wm, w, g.K, g.N, moe::kWsBoxRows))
-    return moe::cuda_status(cudaErrorInvalidValue);
-  for (int m0 = 0; m0 < rows && s == MOE_OK; m0 += 32) {
-    g.M = rows - m0 < 32 ? rows - m0 : 32;
-    g.a = static_cast<const uint8_t*>(a) + (size_t)m0 * g.K;
-    g.sa = a_scales + (size_t)m0 * g.kb;
-    g.out = static_cast<uint8_t*>(out) + (size_t)m0 * ldo * (f32 ? 4 : 2);
-    s = moe::cuda_status(g.M <= 16 ? moe::launch_rows<16>(wm, g, ctas, st)
-                                   : moe::launch_rows<32>(wm, g, ctas, st));
-  }
-  return s;
+  g.a = static_cast<const uint8_t*>(a);
+  g.sa = a_scales;
+  g.out = out;
+  g.M = rows;
+  const int ctas = sms < moe::kProductCtas ? sms : moe::kProductCtas;
+  return moe::cuda_status(rows > moe::kProductRows ? moe::launch_product_tiles(g, sms, st)
+                          : rows > 16             ? moe::launch_rows<32>(g, ctas, st)
+                                                  : moe::launch_rows<16>(g, ctas, st));
 }
 
 MOE_EXPORT moe_status moe_product_device_status(moe_product_t product, void* workspace,

@@ -1,0 +1,535 @@
+// out = A W^T with e4m3 operands and fp32 block scales, more rows than weight_stream.cuh takes:
+//
+//   out[m, n] = sum_kb sa[m, kb] * sw[n / 128, kb] * sum_{k in kb} a[m, k] * w[n, k]
+//
+// The scale changes every 128 K, and arbitrary fp32 scales cannot be given to the tensor
+// core's block-scaled kinds (they take powers of two), so each block of 128 K is multiplied
+// into one of two tensor-memory buffers (exact products, fp32 sums), and the epilogue warps
+// add it to fp32 registers with its scale.
+//
+// A tile is 256 rows x 256 features, by the two CTAs of a cluster with cta_group::2 MMAs: each
+// stages its own 128 rows of A and one half (128 rows) of the weights, 32 KB of shared
+// memory a block, and receives its 128 rows x 256 columns in its own tensor memory.  (A
+// one-CTA 128 x 256 tile stages 48 KB and ran its MMAs at 57 % of the tensor core's rate
+// even without any scales.)  The even CTA issues the MMAs and owns the stage barriers; the
+// odd CTA's loads complete there, and its epilogue warps return buffers by remote arrivals.
+// No load is multicast.
+//
+// Warpgroup 0: TMA producer, MMA issuer; warpgroups 1 and 2 (8 warps) promote and finish,
+// with the registers warpgroup 0 gives back: a thread has one row (its tensor-memory lane)
+// and 128 columns.
+//
+// Fewer tiles than cluster pairs: K is cut into `splits` parts of a tile; each part stores its
+// sums, and the last of a tile's parts to arrive adds all of them in order, so results do not
+// depend on timing.
+#include <cudaTypedefs.h>
+
+#include "product.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int BM = 128;                        // rows of A per CTA
+constexpr int BN = 256;                        // features per tile; half of them staged per CTA
+constexpr int BK = 128;                        // e4m3 values (bytes) per K block
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 384;
+// 12 warps leave each SM sub-partition three: 168 registers a thread at launch.  Warpgroup 0
+// drops to 56, warpgroups 1 and 2 rise to 224: 128 * 56 + 256 * 224 = 384 * 168.
+constexpr int kLaunchRegs = 168;
+constexpr int kProducerRegs = 56;
+constexpr int kEpilogueRegs = 224;
+static_assert(128 * kProducerRegs + 256 * kEpilogueRegs == kThreads * kLaunchRegs,
+              "register shares must add up to the launch's registers");
+constexpr int A_BYTES = BM * BK;
+constexpr int B_BYTES = (BN / 2) * BK;
+constexpr int STAGES = 6;
+constexpr int STG_BYTES = 8 * 256;             // a warp's staged output: 8 rows x 256 bytes
+constexpr unsigned long long kTeardownNs = 100000000ull;
+
+struct TileSmem {
+  alignas(1024) uint8_t a[STAGES][A_BYTES];
+  alignas(1024) uint8_t b[STAGES][B_BYTES];
+  alignas(16) uint8_t stg[kEpiWarps][STG_BYTES];
+  uint64_t full[STAGES];                       // even CTA: stage loaded in both CTAs
+  uint64_t empty[STAGES];                      // stage consumed by the pair's MMAs
+  uint64_t pfull[2];                           // buffer written (both CTAs)
+  uint64_t pempty[2];                          // even CTA: buffer read by all 16 epilogue warps
+  uint64_t teardown;
+  uint32_t tmem;
+  int flag;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Address of the same shared-memory object in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t smem_addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr), "r"(rank));
+  return r;
+}
+// Remote arrival that publishes no memory: it returns a tensor-memory buffer, whose reads
+// tcgen05.wait::ld has completed and tcgen05.fence::before_thread_sync has ordered before.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 2-D tiled TMA load (no multicast) into this CTA's shared memory whose bytes complete on an
+// mbarrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m, int x, int y,
+                                              uint32_t bar_cluster, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar_cluster), "l"(policy)
+      : "memory");
+}
+// D[tmem of both CTAs] (+)= A[smem of both] * B[smem of both]^T, M = 256, N = 256.
+__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t accumulate) {
+  constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) |
+                             ((uint32_t)(2 * BM >> 4) << 24);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on the mbarrier at this offset in both CTAs once the pair MMAs issued so far are done.
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(bar), "h"((uint16_t)0x3)
+      : "memory");
+}
+
+// A scale fetched ahead of its use: the asm keeps the load where it is written.
+__device__ __forceinline__ float ldg_ahead(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
+// Two 16-column TMEM loads without a wait, and the wait that ties the registers of two such
+// pairs: no use of r or q can be scheduled before it.
+__device__ __forceinline__ void tmem_ld_2x16(uint32_t a0, uint32_t a1, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, "
+      "%25, %26, %27, %28, %29, %30, %31}, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a0), "r"(a1)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait2(uint32_t (&r)[32], uint32_t (&q)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31]), "+r"(q[0]), "+r"(q[1]), "+r"(q[2]), "+r"(q[3]),
+                 "+r"(q[4]), "+r"(q[5]), "+r"(q[6]), "+r"(q[7]), "+r"(q[8]), "+r"(q[9]),
+                 "+r"(q[10]), "+r"(q[11]), "+r"(q[12]), "+r"(q[13]), "+r"(q[14]), "+r"(q[15]),
+                 "+r"(q[16]), "+r"(q[17]), "+r"(q[18]), "+r"(q[19]), "+r"(q[20]), "+r"(q[21]),
+                 "+r"(q[22]), "+r"(q[23]), "+r"(q[24]), "+r"(q[25]), "+r"(q[26]), "+r"(q[27]),
+                 "+r"(q[28]), "+r"(q[29]), "+r"(q[30]), "+r"(q[31])
+               :
+               : "memory");
+}
+
+// acc[base .. base + 15] += s * (32 loaded columns, as 16 pairs); a pair is one packed FMA
+__device__ __forceinline__ void promote16(float2 (&acc)[64], int base, const uint32_t (&r)[32],
+                                          float2 s) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    acc[base + c] = __ffma2_rn(make_float2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])),
+                               s, acc[base + c]);
+}
+
+struct TileArgs {
+  ProductArgs p;
+  int tiles_m, splits, kb_per_split, total;    // total = tiles * splits items
+};
+
+struct Item {
+  int tile, split, m0, n0, kb0, kb1;
+};
+__device__ __forceinline__ Item item_of(int i, const TileArgs& t) {
+  Item o;
+  o.tile = i / t.splits;
+  o.split = i - o.tile * t.splits;
+  const int f = o.tile / t.tiles_m;            // feature tile outer, row tile inner
+  o.n0 = f * BN;
+  o.m0 = (o.tile - f * t.tiles_m) * 2 * BM;
+  o.kb0 = o.split * t.kb_per_split;
+  o.kb1 = min(t.p.kb, o.kb0 + t.kb_per_split);
+  return o;
+}
+
+// A warp's 32 rows (m0 ..) x 128 columns (n0 ..) out, 256 bytes of a row at a time: the lanes of
+// 8 rows put their segments into shared memory (16-byte chunk c of row j at slot c ^ j: no bank
+// conflicts either way), then every store instruction covers two whole segments, lanes 0 - 15
+// one row, 16 - 31 the next.  `get(c)`: columns 2c, 2c + 1 of this lane's row.
+template <typename OT, class G>
+__device__ __forceinline__ void store_rows(const ProductArgs& p, uint8_t* stg, int m0, int n0,
+                                           G&& get) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kVals = 256 / sizeof(OT);      // columns of a segment
+  const uint32_t s = smem_u32(stg);
+  OT* out = static_cast<OT*>(p.out);
+  const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && (p.ldo * sizeof(OT)) % 16 == 0;
+#pragma unroll
+  for (int c0 = 0; c0 < 128; c0 += kVals) {
+    uint32_t pk[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+      if (sizeof(OT) == 2) {
+        const float2 v = get(i);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+        pk[i] = *reinterpret_cast<const uint32_t*>(&b);
+      } else {
+        const float2 v = get((c0 + i) / 2);
+        pk[i] = __float_as_uint((i & 1) ? v.y : v.x);
+      }
+    }
+#pragma unroll 1
+    for (int rnd = 0; rnd < 4; ++rnd) {
+      if (m0 + 8 * rnd >= p.M) break;
+      if ((lane >> 3) == rnd) {
+        const int j = lane & 7;
+#pragma unroll
+        for (int w = 0; w < 16; ++w)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(s + j * 256 +
+                                                                        ((w ^ j) & 15) * 16),
+                       "r"(pk[4 * w]), "r"(pk[4 * w + 1]), "r"(pk[4 * w + 2]), "r"(pk[4 * w + 3])
+                       : "memory");
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = 2 * i + (lane >> 4), c = lane & 15;
+        uint4 o;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                     : "r"(s + j * 256 + ((c ^ j) & 15) * 16)
+                     : "memory");
+        const int m = m0 + rnd * 8 + j, n = n0 + c0 + c * (16 / (int)sizeof(OT));
+        if (m < p.M && n < p.N) {
+          OT* dst = out + m * p.ldo + n;
+          if (vec && n + 16 / (int)sizeof(OT) <= p.N) {
+            *reinterpret_cast<uint4*>(dst) = o;
+          } else {
+            const OT* v = reinterpret_cast<const OT*>(&o);
+#pragma unroll
+            for (int e = 0; e < 16 / (int)sizeof(OT); ++e)
+              if (n + e < p.N) dst[e] = v[e];
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
+template <bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    product_tiles_kernel(const __grid_constant__ CUtensorMap tmA,
+                         const __grid_constant__ CUtensorMap tmW, const TileArgs t) {
+  extern __shared__ uint8_t smem_raw[];
+  TileSmem& s = *reinterpret_cast<TileSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const ProductArgs& p = t.p;
+  constexpr unsigned int kBit = MOE_DEV_WAIT_TIMEOUT_PRODUCT;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();          // 0: issues the MMAs
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.pfull[i]), 1);
+      mbar_init(smem_u32(&s.pempty[i]), 2 * kEpiWarps);
+    }
+    mbar_init(smem_u32(&s.teardown), 1);
+    fence_mbarrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmW);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&s.tmem)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();        // the peer's barriers are initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = s.tmem;
+
+  if (warp < 4) {
+    regs_dec<kProducerRegs>();
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ TMA producer
+      const uint64_t pol = policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, parity = 0;
+      bool ok = true;
+      const uint32_t full0 = map_to_rank(smem_u32(&s.full[0]), 0);   // the even CTA's barriers
+      for (int i = pair; i < t.total && ok; i += npairs) {
+        const Item it = item_of(i, t);
+        const int arow = it.m0 + BM * (int)rank, wrow = it.n0 + (BN / 2) * (int)rank;
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+          if (!mbar_wait_sleep(smem_u32(&s.empty[stage]), phase ^ 1u, p.wait_limit_ns, p.status,
+                               kBit)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s.full[stage]), 2 * (A_BYTES + B_BYTES));
+          const uint32_t fb = full0 + stage * (uint32_t)sizeof(uint64_t);
+          tma_load_pair(smem_u32(s.a[stage]), &tmA, kb * BK, arow, fb, pol);
+          tma_load_pair(smem_u32(s.b[stage]), &tmW, kb * BK, wrow, fb, pol);
+          issued |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // no load may still be writing when the CTA leaves: wait until the MMAs have consumed the
+      // last load of every stage (which follows its arrival)
+      for (int i = 0; i < STAGES; ++i)
+        if ((issued >> i) & 1u)
+          mbar_wait_sleep(smem_u32(&s.empty[i]), (parity >> i) & 1u, kTeardownNs, p.status, kBit);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // -------------------------------------------------------------- MMA issuer
+      int stage = 0;
+      uint32_t phase = 0, kcount = 0;
+      bool ok = true, any = false;
+      for (int i = pair; i < t.total && ok; i += npairs) {
+        const Item it = item_of(i, t);
+        for (int kb = it.kb0; kb < it.kb1; ++kb, ++kcount) {
+          const uint32_t pb = kcount & 1u, use = kcount >> 1;
+          if (!mbar_wait_bounded(smem_u32(&s.pempty[pb]), (use & 1u) ^ 1u, p.wait_limit_ns,
+                                 p.status, kBit) ||
+              !mbar_wait_bounded(smem_u32(&s.full[stage]), phase, p.wait_limit_ns, p.status,
+                                 kBit)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t a = smem_desc_sw128(smem_u32(s.a[stage]));
+          const uint64_t b = smem_desc_sw128(smem_u32(s.b[stage]));
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)   // +32 bytes per K step = 2 in the address field
+            umma_pair(tmem + pb * BN, a + 2 * k, b + 2 * k, k != 0);
+          umma_commit_pair(smem_u32(&s.empty[stage]));
+          umma_commit_pair(smem_u32(&s.pfull[pb]));
+          any = true;
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (any) {
+        umma_commit_pair(smem_u32(&s.teardown));
+        mbar_wait_sleep(smem_u32(&s.teardown), 0, kTeardownNs, p.status, kBit);
+      }
+    } else if (warp == 1 && lane == 0) {
+      // odd CTA: the pair's last MMAs before tensor memory is freed
+      if (pair < t.total)
+        mbar_wait_sleep(smem_u32(&s.teardown), 0, kTeardownNs, p.status, kBit);
+    }
+    __syncwarp();
+  } else {
+    regs_inc<kEpilogueRegs>();
+    // ---------------------------------------------------- promotion and epilogue
+    // After an expired wait the warps keep walking without further waits, so that every named
+    // barrier is reached.
+    const int q = warp & 3, hh = (warp - 4) >> 2;   // tensor-memory lanes, column half
+    const uint32_t pempty[2] = {map_to_rank(smem_u32(&s.pempty[0]), 0),
+                                map_to_rank(smem_u32(&s.pempty[1]), 0)};
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + hh * 128;
+    uint32_t kcount = 0;
+    bool ok = true;
+    for (int i = pair; i < t.total; i += npairs) {
+      const Item it = item_of(i, t);
+      const int m0 = it.m0 + BM * (int)rank + q * 32, n0 = it.n0 + hh * 128;
+      const bool warp_live = m0 < p.M && n0 < p.N;
+      // rows and columns past the end read the last ones' scales (in bounds, not used)
+      const float* sa = p.sa + (size_t)min(m0 + lane, p.M - 1) * p.kb;
+      const float* sw = p.sw + (size_t)(min(n0, p.N - 1) / 128) * p.kb;
+      float2 acc[64];
+#pragma unroll
+      for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
+      // scales two blocks ahead, one set for even and one for odd blocks
+      float xa[2] = {ldg_ahead(sa + it.kb0), 0.f}, xw[2] = {ldg_ahead(sw + it.kb0), 0.f};
+      if (it.kb0 + 1 < it.kb1) {
+        xa[1] = ldg_ahead(sa + it.kb0 + 1);
+        xw[1] = ldg_ahead(sw + it.kb0 + 1);
+      }
+      for (int kk = it.kb0; kk < it.kb1; kk += 2) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int kb = kk + j;
+          if (kb >= it.kb1) break;
+          const uint32_t pb = kcount & 1u, use = kcount >> 1;
+          ++kcount;
+          if (ok)
+            ok = mbar_wait_bounded_warp(smem_u32(&s.pfull[pb]), use & 1u, p.wait_limit_ns, p.status,
+                                        kBit);
+          const float f = xa[j] * xw[j];
+          if (kb + 2 < it.kb1) {
+            xa[j] = ldg_ahead(sa + kb + 2);
+            xw[j] = ldg_ahead(sw + kb + 2);
+          }
+          if (!ok) continue;
+          tc_fence_after();
+          auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(pb ? pempty[1] : pempty[0]);
+          };
+          if (warp_live) {
+            const uint32_t at = lanes + pb * BN;
+            const float2 f2 = make_float2(f, f);
+            uint32_t ra[32], rb[32];
+            tmem_ld_2x16(at, at + 16, ra);
+            tmem_ld_2x16(at + 32, at + 48, rb);
+            tmem_ld_wait2(ra, rb);
+            promote16(acc, 0, ra, f2);
+            promote16(acc, 16, rb, f2);
+            tmem_ld_2x16(at + 64, at + 80, ra);
+            tmem_ld_2x16(at + 96, at + 112, rb);
+            tmem_ld_wait2(ra, rb);
+            release();
+            promote16(acc, 32, ra, f2);
+            promote16(acc, 48, rb, f2);
+          } else {
+            release();
+          }
+        }
+      }
+      bool finish = true;
+      const int et = threadIdx.x - 128;               // epilogue thread
+      // this CTA's partial sums of a part of the tile: [column / 4][thread][4]
+      auto part_of = [&](int sp) {
+        return reinterpret_cast<float4*>(p.part) +
+               ((size_t)(it.tile * t.splits + sp) * 2 + rank) * (32 * 256) + et;
+      };
+      if (t.splits > 1) {
+        float4* o = part_of(it.split);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          o[c * 256] = make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y);
+        named_bar_sync(1, kEpiWarps * 32);
+        if (et == 0) {
+          unsigned int* counter = p.counters + it.tile * 2 + rank;
+          unsigned int v;
+          asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                       : "=r"(v)
+                       : "l"(counter)
+                       : "memory");
+          s.flag = v + 1 == (unsigned int)t.splits;
+          if (s.flag) *counter = 0;
+        }
+        named_bar_sync(1, kEpiWarps * 32);
+        finish = s.flag != 0;
+        if (finish) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
+          for (int sp = 0; sp < t.splits; ++sp) {
+            const float4* o2 = part_of(sp);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float4 v = __ldcg(o2 + c * 256);
+              acc[2 * c].x += v.x;
+              acc[2 * c].y += v.y;
+              acc[2 * c + 1].x += v.z;
+              acc[2 * c + 1].y += v.w;
+            }
+          }
+        }
+      }
+      if (finish && ok && warp_live) {
+        auto get = [&](int c) { return acc[c]; };
+        if (F32)
+          store_rows<float>(p, s.stg[warp - 4], m0, n0, get);
+        else
+          store_rows<__nv_bfloat16>(p, s.stg[warp - 4], m0, n0, get);
+      }
+    }
+  }
+
+  // Neither CTA leaves (or frees tensor memory) while the other may still arrive on its
+  // barriers or have the tensor core read its shared memory.
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+  }
+}
+
+// The register shares of the warpgroups only add up if the kernel was built with exactly
+// kLaunchRegs registers a thread; anything else is refused rather than launched (a
+// mismatched split would wait forever).
+template <bool F32>
+cudaError_t prepare() {
+  static_assert(sizeof(TileSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");
+  cudaFuncAttributes attr;
+  cudaError_t e = cudaFuncGetAttributes(&attr, product_tiles_kernel<F32>);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(product_tiles_kernel<F32>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)sizeof(TileSmem) + 1024);
+}
+
+}  // namespace
+
+cudaError_t prepare_product_tiles() {
+  const cudaError_t e = prepare<false>();
+  return e == cudaSuccess ? prepare<true>() : e;
+}
+
+cudaError_t launch_product_tiles(const ProductArgs& p, int num_sms, cudaStream_t st) {
+  CUtensorMap ma, mw;
+  if (!ws_map(&ma, p.a, p.K, p.M, BM) || !ws_map(&mw, p.w, p.K, p.N, BN / 2))
+    return cudaErrorInvalidValue;
+  TileArgs t;
+  t.p = p;
+  t.tiles_m = (p.M + 2 * BM - 1) / (2 * BM);
+  const long long tiles = (long long)t.tiles_m * ((p.N + BN - 1) / BN);
+  if (tiles > (1 << 29)) return cudaErrorInvalidValue;
+  const int pairs = num_sms / 2 < kProductPairs ? num_sms / 2 : kProductPairs;
+  // A part of a tile costs a store and a load of its sums, about what four blocks take.
+  int splits = tiles < pairs ? pairs / (int)tiles : 1;
+  if (splits > p.kb / 4) splits = p.kb / 4;
+  if (splits < 1) splits = 1;
+  t.kb_per_split = (p.kb + splits - 1) / splits;
+  t.splits = (p.kb + t.kb_per_split - 1) / t.kb_per_split;
+  t.total = (int)tiles * t.splits;
+  const int grid = 2 * (t.total < pairs ? t.total : pairs);
+  if (p.f32)
+    product_tiles_kernel<true><<<grid, kThreads, sizeof(TileSmem) + 1024, st>>>(ma, mw, t);
+  else
+    product_tiles_kernel<false><<<grid, kThreads, sizeof(TileSmem) + 1024, st>>>(ma, mw, t);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

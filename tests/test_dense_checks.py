@@ -31,6 +31,9 @@ class Fake(FakeCuda):
     def stride(self, d):
         return (self.ld, 1)[d]
 
+    def get_device(self):
+        return 0
+
 
 @pytest.mark.parametrize("wtype", [moe.MOE_W_BF16, moe.MOE_W_FP8_E4M3_B128])
 def test_few_rejects_before_launch(lib, wtype):
