@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   using S = decltype(s.ws);
   constexpr int EB = FP8 ? 1 : 2;                     // bytes of a weight
-  const int warp = threadIdx.x >> 5;
+  const int warp = warp_index();
   const int ch_h = p.H * EB / kWsBytes;               // stages of a gate/up tile
   const int ch_i = p.I * EB / kWsBytes;               // stages of a slot of a down tile
   const int ch_s = p.S ? p.Is * EB / kWsBytes : 0;
@@ -627,7 +627,8 @@ cudaError_t prepare() {
 
 }  // namespace
 
-bool ws_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64_t rows, int box_rows) {
+bool ws_map_nd(CUtensorMap* m, const void* w, int rank, const uint64_t* dims,
+               const uint64_t* strides, const uint32_t* box) {
   static const auto encode = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -638,14 +639,24 @@ bool ws_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64_t rows, in
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }();
   if (encode == nullptr) return false;
-  const cuuint64_t dims[2] = {row_bytes, rows};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(w), dims, strides, box,
-                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  cuuint64_t d[5], st[5];
+  cuuint32_t b[5], one[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    one[i] = 1;
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(w), d, st, b,
+                one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool ws_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64_t rows, int box_rows) {
+  const uint64_t dims[2] = {row_bytes, rows};
+  const uint32_t box[2] = {128, (uint32_t)box_rows};
+  return ws_map_nd(m, w, 2, dims, &row_bytes, box);
 }
 
 cudaError_t prepare_few_kernels() {

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kWsBlock, 1)
   RowsSmem<ROWS>& s = *reinterpret_cast<RowsSmem<ROWS>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   using S = decltype(s.ws);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
   const int per = p.kb;                               // stages of a tile
   const WsSplit split((p.N + kWsRows - 1) / kWsRows, per, ctas);

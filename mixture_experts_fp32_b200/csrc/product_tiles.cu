@@ -4,8 +4,13 @@
 //
 // The scale changes every 128 K, and arbitrary fp32 scales cannot be given to the tensor
 // core's block-scaled kinds (they take powers of two), so each block of 128 K is multiplied
-// into one of two tensor-memory buffers (exact products, fp32 sums), and the epilogue warps
-// add it to fp32 registers with its scale.
+// into tensor-memory buffers of its own (exact products, fp32 sums), and the epilogue warps
+// add them to fp32 registers with its scale.  That is what bounds the kernel: a block's
+// MMAs take 512 clocks, its FMAs 290, and its way through tensor memory more than either (about
+// 900 clocks from an MMA's issue until its completion is seen, 500 until the buffer has been
+// read and returned).  So the two warpgroups of the epilogue have a half of the features each
+// and two buffers of their own for it: while one waits for its half or reads it, the other
+// adds.  (One pair of buffers for both: 880 clocks a block.)
 //
 // A tile is 256 rows x 256 features, by the two CTAs of a cluster with cta_group::2 MMAs: each
 // stages its own 128 rows of A and one half (128 rows) of the weights, 32 KB of shared
@@ -14,6 +19,10 @@
 // even without any scales.)  The even CTA issues the MMAs and owns the stage barriers; the
 // odd CTA's loads complete there, and its epilogue warps return buffers by remote arrivals.
 // No load is multicast.
+//
+// A stage is two K blocks, which one TMA instruction brings for A and one for W (a 3-D map of
+// 128-byte columns; where K is no multiple of 128 the last column has no 128 bytes, and two
+// 2-D loads take the place of each).
 //
 // Warpgroup 0: TMA producer, MMA issuer; warpgroups 1 and 2 (8 warps) promote and finish,
 // with the registers warpgroup 0 gives back: a thread has one row (its tensor-memory lane)
@@ -31,30 +40,31 @@ namespace {
 
 constexpr int BM = 128;                        // rows of A per CTA
 constexpr int BN = 256;                        // features per tile; half of them staged per CTA
+constexpr int BH = BN / 2;                     // features of a half: 64 of them staged per CTA
 constexpr int BK = 128;                        // e4m3 values (bytes) per K block
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 384;
 // 12 warps leave each SM sub-partition three: 168 registers a thread at launch.  Warpgroup 0
-// drops to 56, warpgroups 1 and 2 rise to 224: 128 * 56 + 256 * 224 = 384 * 168.
+// drops to 24, warpgroups 1 and 2 rise to 240: 128 * 24 + 256 * 240 = 384 * 168.
 constexpr int kLaunchRegs = 168;
-constexpr int kProducerRegs = 56;
-constexpr int kEpilogueRegs = 224;
+constexpr int kProducerRegs = 24;
+constexpr int kEpilogueRegs = 240;
 static_assert(128 * kProducerRegs + 256 * kEpilogueRegs == kThreads * kLaunchRegs,
               "register shares must add up to the launch's registers");
 constexpr int A_BYTES = BM * BK;
 constexpr int B_BYTES = (BN / 2) * BK;
-constexpr int STAGES = 6;
+constexpr int STAGES = 3;                      // of two K blocks
 constexpr int STG_BYTES = 8 * 256;             // a warp's staged output: 8 rows x 256 bytes
 constexpr unsigned long long kTeardownNs = 100000000ull;
 
 struct TileSmem {
-  alignas(1024) uint8_t a[STAGES][A_BYTES];
-  alignas(1024) uint8_t b[STAGES][B_BYTES];
+  alignas(1024) uint8_t a[STAGES][2 * A_BYTES];
+  alignas(1024) uint8_t b[STAGES][2 * B_BYTES];   // [half][K block][64 rows]
   alignas(16) uint8_t stg[kEpiWarps][STG_BYTES];
   uint64_t full[STAGES];                       // even CTA: stage loaded in both CTAs
   uint64_t empty[STAGES];                      // stage consumed by the pair's MMAs
-  uint64_t pfull[2];                           // buffer written (both CTAs)
-  uint64_t pempty[2];                          // even CTA: buffer read by all 16 epilogue warps
+  uint64_t pfull[2][2];                        // [half][buffer] written (both CTAs)
+  uint64_t pempty[2][2];                        // even CTA: buffer read by its 8 epilogue warps
   uint64_t teardown;
   uint32_t tmem;
   int flag;
@@ -90,10 +100,18 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar_cluster), "l"(policy)
       : "memory");
 }
-// D[tmem of both CTAs] (+)= A[smem of both] * B[smem of both]^T, M = 256, N = 256.
+__device__ __forceinline__ void tma_load_pair_3d(uint32_t dst, const CUtensorMap* m, int y, int z,
+                                                 uint32_t bar_cluster, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(y), "r"(z), "r"(bar_cluster), "l"(policy)
+      : "memory");
+}
+// D[tmem of both CTAs] (+)= A[smem of both] * B[smem of both]^T, M = 256, N = 128.
 __device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                           uint32_t accumulate) {
-  constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) |
+  constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BH >> 3) << 17) |
                              ((uint32_t)(2 * BM >> 4) << 24);
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -160,7 +178,8 @@ __device__ __forceinline__ void promote16(float2 (&acc)[64], int base, const uin
 
 struct TileArgs {
   ProductArgs p;
-  int tiles_m, splits, kb_per_split, total;    // total = tiles * splits items
+  int tiles_m, splits, kb_per_split, total;    // total = tiles * splits items; kb_per_split even
+  bool columns;                                // maps of 128-byte columns (K a multiple of 128)
 };
 
 struct Item {
@@ -187,6 +206,7 @@ __device__ __forceinline__ void store_rows(const ProductArgs& p, uint8_t* stg, i
                                            G&& get) {
   const int lane = threadIdx.x & 31;
   constexpr int kVals = 256 / sizeof(OT);      // columns of a segment
+  constexpr int kChunk = 16 / sizeof(OT);      // and of a 16-byte chunk
   const uint32_t s = smem_u32(stg);
   OT* out = static_cast<OT*>(p.out);
   const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && (p.ldo * sizeof(OT)) % 16 == 0;
@@ -217,24 +237,40 @@ __device__ __forceinline__ void store_rows(const ProductArgs& p, uint8_t* stg, i
                        : "memory");
       }
       __syncwarp();
+      if (vec) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = 2 * i + (lane >> 4), c = lane & 15;
-        uint4 o;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
-                     : "r"(s + j * 256 + ((c ^ j) & 15) * 16)
-                     : "memory");
-        const int m = m0 + rnd * 8 + j, n = n0 + c0 + c * (16 / (int)sizeof(OT));
-        if (m < p.M && n < p.N) {
-          OT* dst = out + m * p.ldo + n;
-          if (vec && n + 16 / (int)sizeof(OT) <= p.N) {
-            *reinterpret_cast<uint4*>(dst) = o;
-          } else {
-            const OT* v = reinterpret_cast<const OT*>(&o);
+        for (int i = 0; i < 4; ++i) {
+          const int j = 2 * i + (lane >> 4), c = lane & 15;
+          uint4 o;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                       : "r"(s + j * 256 + ((c ^ j) & 15) * 16)
+                       : "memory");
+          const int m = m0 + rnd * 8 + j, n = n0 + c0 + c * kChunk;
+          if (m < p.M && n < p.N) {
+            OT* dst = out + m * p.ldo + n;
+            if (n + kChunk <= p.N) {
+              *reinterpret_cast<uint4*>(dst) = o;
+            } else {
+              const OT* v = reinterpret_cast<const OT*>(&o);
 #pragma unroll
-            for (int e = 0; e < 16 / (int)sizeof(OT); ++e)
-              if (n + e < p.N) dst[e] = v[e];
+              for (int e = 0; e < kChunk; ++e)
+                if (n + e < p.N) dst[e] = v[e];
+            }
+          }
+        }
+      } else {
+        // rows that begin anywhere: consecutive lanes store consecutive values
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+          const int m = m0 + rnd * 8 + j;
+          if (m >= p.M) break;
+#pragma unroll
+          for (int e = lane; e < kVals; e += 32) {
+            const int c = e / kChunk, n = n0 + c0 + e;
+            if (n < p.N)
+              out[m * p.ldo + n] = reinterpret_cast<const OT*>(
+                  stg + j * 256 + ((c ^ j) & 15) * 16)[e % kChunk];
           }
         }
       }
@@ -252,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                              ~uintptr_t(1023));
   const ProductArgs& p = t.p;
   constexpr unsigned int kBit = MOE_DEV_WAIT_TIMEOUT_PRODUCT;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();          // 0: issues the MMAs
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
@@ -261,9 +297,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&s.full[i]), 1);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&s.pfull[i]), 1);
-      mbar_init(smem_u32(&s.pempty[i]), 2 * kEpiWarps);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&s.pfull[i >> 1][i & 1]), 1);
+      mbar_init(smem_u32(&s.pempty[i >> 1][i & 1]), kEpiWarps);   // four of either CTA
     }
     mbar_init(smem_u32(&s.teardown), 1);
     fence_mbarrier_init();
@@ -281,11 +317,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync_all();        // the peer's barriers are initialised before any remote arrival
   tc_fence_after();
-  const uint32_t tmem = s.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
 
   if (warp < 4) {
     regs_dec<kProducerRegs>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
       const uint64_t pol = policy_evict_normal();
       int stage = 0;
@@ -294,17 +330,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t full0 = map_to_rank(smem_u32(&s.full[0]), 0);   // the even CTA's barriers
       for (int i = pair; i < t.total && ok; i += npairs) {
         const Item it = item_of(i, t);
-        const int arow = it.m0 + BM * (int)rank, wrow = it.n0 + (BN / 2) * (int)rank;
-        for (int kb = it.kb0; kb < it.kb1; ++kb) {
-          if (!mbar_wait_sleep(smem_u32(&s.empty[stage]), phase ^ 1u, p.wait_limit_ns, p.status,
-                               kBit)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s.full[stage]), 2 * (A_BYTES + B_BYTES));
+        const int arow = it.m0 + BM * (int)rank, wrow = it.n0 + (BH / 2) * (int)rank;
+        for (int kb = it.kb0; kb < it.kb1; kb += 2) {
+          ok = ws_wait(smem_u32(&s.empty[stage]), phase ^ 1u, p.wait_limit_ns,
+                                      p.status, kBit);
+          if (!ok) break;
+          const uint32_t own = smem_u32(&s.full[stage]);
           const uint32_t fb = full0 + stage * (uint32_t)sizeof(uint64_t);
-          tma_load_pair(smem_u32(s.a[stage]), &tmA, kb * BK, arow, fb, pol);
-          tma_load_pair(smem_u32(s.b[stage]), &tmW, kb * BK, wrow, fb, pol);
+          const uint32_t a = smem_u32(s.a[stage]), b = smem_u32(s.b[stage]);
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(own, 4 * (A_BYTES + B_BYTES));
+            if (t.columns) {
+              tma_load_pair_3d(a, &tmA, arow, kb, fb, pol);
+              tma_load_pair_3d(b, &tmW, wrow, kb, fb, pol);
+              tma_load_pair_3d(b + B_BYTES, &tmW, wrow + BH, kb, fb, pol);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {           // past the end of K: zeros
+                tma_load_pair(a + j * A_BYTES, &tmA, (kb + j) * BK, arow, fb, pol);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  tma_load_pair(b + h * B_BYTES + j * (B_BYTES / 2), &tmW, (kb + j) * BK,
+                                wrow + h * BH, fb, pol);
+              }
+            }
+          }
+          __syncwarp();
           issued |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -314,43 +365,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // last load of every stage (which follows its arrival)
       for (int i = 0; i < STAGES; ++i)
         if ((issued >> i) & 1u)
-          mbar_wait_sleep(smem_u32(&s.empty[i]), (parity >> i) & 1u, kTeardownNs, p.status, kBit);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+          mbar_wait_sleep_warp(smem_u32(&s.empty[i]), (parity >> i) & 1u, kTeardownNs, p.status,
+                               kBit);
+    } else if (warp == 1 && rank == 0) {
       // -------------------------------------------------------------- MMA issuer
       int stage = 0;
-      uint32_t phase = 0, kcount = 0;
+      uint32_t phase = 0, count = 0;
       bool ok = true, any = false;
       for (int i = pair; i < t.total && ok; i += npairs) {
         const Item it = item_of(i, t);
-        for (int kb = it.kb0; kb < it.kb1; ++kb, ++kcount) {
-          const uint32_t pb = kcount & 1u, use = kcount >> 1;
-          if (!mbar_wait_bounded(smem_u32(&s.pempty[pb]), (use & 1u) ^ 1u, p.wait_limit_ns,
-                                 p.status, kBit) ||
-              !mbar_wait_bounded(smem_u32(&s.full[stage]), phase, p.wait_limit_ns, p.status,
-                                 kBit)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        for (int kb = it.kb0; kb < it.kb1 && ok; kb += 2) {
+          ok = ws_wait(smem_u32(&s.full[stage]), phase, p.wait_limit_ns, p.status,
+                                      kBit);
+          if (!ok) break;
           const uint64_t a = smem_desc_sw128(smem_u32(s.a[stage]));
           const uint64_t b = smem_desc_sw128(smem_u32(s.b[stage]));
+          const int blocks = min(2, it.kb1 - kb);
+          for (int j = 0; j < blocks && ok; ++j, ++count) {
+            const uint32_t pb = count & 1u, use = count >> 1;
+            const uint64_t aj = a + j * (A_BYTES >> 4);
 #pragma unroll
-          for (int k = 0; k < BK / 32; ++k)   // +32 bytes per K step = 2 in the address field
-            umma_pair(tmem + pb * BN, a + 2 * k, b + 2 * k, k != 0);
-          umma_commit_pair(smem_u32(&s.empty[stage]));
-          umma_commit_pair(smem_u32(&s.pfull[pb]));
-          any = true;
+            for (int h = 0; h < 2; ++h) {
+              ok = ok && ws_wait(smem_u32(&s.pempty[h][pb]), (use & 1u) ^ 1u, p.wait_limit_ns,
+                                 p.status, kBit);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t bj = b + (h * B_BYTES + j * (B_BYTES / 2) >> 4);
+              const uint32_t dst = tmem + (2 * h + pb) * BH, full = smem_u32(&s.pfull[h][pb]);
+              const uint32_t empty = smem_u32(&s.empty[stage]);
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < BK / 32; ++k)   // +32 bytes per K step = 2 in the address field
+                  umma_pair(dst, aj + 2 * k, bj + 2 * k, k != 0);
+                umma_commit_pair(full);
+                if (h == 1 && j + 1 == blocks) umma_commit_pair(empty);
+              }
+              __syncwarp();
+              any = true;
+            }
+          }
+          if (!ok) break;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
       if (any) {
-        umma_commit_pair(smem_u32(&s.teardown));
-        mbar_wait_sleep(smem_u32(&s.teardown), 0, kTeardownNs, p.status, kBit);
+        if (elect_one()) umma_commit_pair(smem_u32(&s.teardown));
+        __syncwarp();
+        mbar_wait_sleep_warp(smem_u32(&s.teardown), 0, kTeardownNs, p.status, kBit);
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // odd CTA: the pair's last MMAs before tensor memory is freed
       if (pair < t.total)
-        mbar_wait_sleep(smem_u32(&s.teardown), 0, kTeardownNs, p.status, kBit);
+        mbar_wait_sleep_warp(smem_u32(&s.teardown), 0, kTeardownNs, p.status, kBit);
     }
     __syncwarp();
   } else {
@@ -359,69 +425,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // After an expired wait the warps keep walking without further waits, so that every named
     // barrier is reached.
     const int q = warp & 3, hh = (warp - 4) >> 2;   // tensor-memory lanes, column half
-    const uint32_t pempty[2] = {map_to_rank(smem_u32(&s.pempty[0]), 0),
-                                map_to_rank(smem_u32(&s.pempty[1]), 0)};
-    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + hh * 128;
-    uint32_t kcount = 0;
+    const uint32_t pempty0 = map_to_rank(smem_u32(&s.pempty[hh][0]), 0);
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + hh * 2 * BH;
+    uint32_t count = 0;
     bool ok = true;
+    // scales two blocks ahead, one set for even and one for odd blocks; an item's first ones are
+    // asked for before the item before it is stored
+    float xa[2], xw[2];
+    const float *sa, *sw;
+    auto first_scales = [&](const Item& it) {
+      // rows and columns past the end read the last ones' scales (in bounds, not used)
+      sa = p.sa + (size_t)min(it.m0 + BM * (int)rank + q * 32 + lane, p.M - 1) * p.kb;
+      sw = p.sw + (size_t)(min(it.n0 + hh * BH, p.N - 1) / 128) * p.kb;
+      const int next = min(it.kb0 + 1, it.kb1 - 1);
+      xa[0] = ldg_ahead(sa + it.kb0);
+      xw[0] = ldg_ahead(sw + it.kb0);
+      xa[1] = ldg_ahead(sa + next);
+      xw[1] = ldg_ahead(sw + next);
+    };
+    if (pair < t.total) first_scales(item_of(pair, t));
     for (int i = pair; i < t.total; i += npairs) {
       const Item it = item_of(i, t);
-      const int m0 = it.m0 + BM * (int)rank + q * 32, n0 = it.n0 + hh * 128;
+      const int m0 = it.m0 + BM * (int)rank + q * 32, n0 = it.n0 + hh * BH;
       const bool warp_live = m0 < p.M && n0 < p.N;
-      // rows and columns past the end read the last ones' scales (in bounds, not used)
-      const float* sa = p.sa + (size_t)min(m0 + lane, p.M - 1) * p.kb;
-      const float* sw = p.sw + (size_t)(min(n0, p.N - 1) / 128) * p.kb;
       float2 acc[64];
 #pragma unroll
       for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
-      // scales two blocks ahead, one set for even and one for odd blocks
-      float xa[2] = {ldg_ahead(sa + it.kb0), 0.f}, xw[2] = {ldg_ahead(sw + it.kb0), 0.f};
-      if (it.kb0 + 1 < it.kb1) {
-        xa[1] = ldg_ahead(sa + it.kb0 + 1);
-        xw[1] = ldg_ahead(sw + it.kb0 + 1);
-      }
       for (int kk = it.kb0; kk < it.kb1; kk += 2) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int kb = kk + j;
           if (kb >= it.kb1) break;
-          const uint32_t pb = kcount & 1u, use = kcount >> 1;
-          ++kcount;
-          if (ok)
-            ok = mbar_wait_bounded_warp(smem_u32(&s.pfull[pb]), use & 1u, p.wait_limit_ns, p.status,
-                                        kBit);
           const float f = xa[j] * xw[j];
+          const float2 f2 = make_float2(f, f);
           if (kb + 2 < it.kb1) {
             xa[j] = ldg_ahead(sa + kb + 2);
             xw[j] = ldg_ahead(sw + kb + 2);
           }
+          const uint32_t pb = count & 1u, use = count >> 1;
+          ++count;
+          if (ok) ok = ws_wait(smem_u32(&s.pfull[hh][pb]), use & 1u, p.wait_limit_ns, p.status, kBit);
           if (!ok) continue;
           tc_fence_after();
-          auto release = [&]() {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(pb ? pempty[1] : pempty[0]);
-          };
+          const uint32_t at = lanes + pb * BH;
+          uint32_t ra[32], rb[32];
           if (warp_live) {
-            const uint32_t at = lanes + pb * BN;
-            const float2 f2 = make_float2(f, f);
-            uint32_t ra[32], rb[32];
+            // half the columns at a time, and the buffer goes back before the last 64 are added:
+            // what an MMA waits for is the buffer
             tmem_ld_2x16(at, at + 16, ra);
             tmem_ld_2x16(at + 32, at + 48, rb);
             tmem_ld_wait2(ra, rb);
             promote16(acc, 0, ra, f2);
-            promote16(acc, 16, rb, f2);
             tmem_ld_2x16(at + 64, at + 80, ra);
+            promote16(acc, 16, rb, f2);
             tmem_ld_2x16(at + 96, at + 112, rb);
             tmem_ld_wait2(ra, rb);
-            release();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (rank == 0) {
+            if (elect_one()) mbar_arrive(smem_u32(&s.pempty[hh][pb]));
+          } else if (elect_one()) {
+            mbar_arrive_remote(pempty0 + pb * (uint32_t)sizeof(uint64_t));
+          }
+          if (warp_live) {
             promote16(acc, 32, ra, f2);
             promote16(acc, 48, rb, f2);
-          } else {
-            release();
           }
         }
       }
+      if (i + npairs < t.total) first_scales(item_of(i + npairs, t));
       bool finish = true;
       const int et = threadIdx.x - 128;               // epilogue thread
       // this CTA's partial sums of a part of the tile: [column / 4][thread][4]
@@ -500,6 +573,13 @@ cudaError_t prepare() {
                               (int)sizeof(TileSmem) + 1024);
 }
 
+// Row-major bytes [rows, K] as [K / 128][rows][128], in boxes of two columns of `box_rows` rows.
+bool column_map(CUtensorMap* m, const void* w, uint64_t K, uint64_t rows, int box_rows) {
+  const uint64_t dims[3] = {BK, rows, K / BK}, strides[2] = {K, BK};
+  const uint32_t box[3] = {BK, (uint32_t)box_rows, 2};
+  return ws_map_nd(m, w, 3, dims, strides, box);
+}
+
 }  // namespace
 
 cudaError_t prepare_product_tiles() {
@@ -508,20 +588,29 @@ cudaError_t prepare_product_tiles() {
 }
 
 cudaError_t launch_product_tiles(const ProductArgs& p, int num_sms, cudaStream_t st) {
-  CUtensorMap ma, mw;
-  if (!ws_map(&ma, p.a, p.K, p.M, BM) || !ws_map(&mw, p.w, p.K, p.N, BN / 2))
-    return cudaErrorInvalidValue;
   TileArgs t;
+  t.columns = p.K % BK == 0;
+  CUtensorMap ma, mw;
+  if (t.columns ? !column_map(&ma, p.a, p.K, p.M, BM) || !column_map(&mw, p.w, p.K, p.N, BH / 2)
+                : !ws_map(&ma, p.a, p.K, p.M, BM) || !ws_map(&mw, p.w, p.K, p.N, BH / 2))
+    return cudaErrorInvalidValue;
   t.p = p;
   t.tiles_m = (p.M + 2 * BM - 1) / (2 * BM);
   const long long tiles = (long long)t.tiles_m * ((p.N + BN - 1) / BN);
   if (tiles > (1 << 29)) return cudaErrorInvalidValue;
   const int pairs = num_sms / 2 < kProductPairs ? num_sms / 2 : kProductPairs;
-  // A part of a tile costs a store and a load of its sums, about what four blocks take.
-  int splits = tiles < pairs ? pairs / (int)tiles : 1;
-  if (splits > p.kb / 4) splits = p.kb / 4;
-  if (splits < 1) splits = 1;
+  // Parts of tiles where there are fewer tiles than pairs.  A block of K takes 900 clocks; joining
+  // parts takes 6000 and 1500 a part (28 tiles of 16 blocks: 21 us whole, 24 us in halves).
+  int splits = 1;
+  if (tiles < pairs) {
+    const auto cost = [&](int n) {
+      return (p.kb + n - 1) / n * 900 + (n > 1 ? 6000 + 1500 * n : 0);
+    };
+    for (int n = 2; n * tiles <= pairs && n <= p.kb; ++n)
+      if (cost(n) < cost(splits)) splits = n;
+  }
   t.kb_per_split = (p.kb + splits - 1) / splits;
+  t.kb_per_split += t.kb_per_split & 1;
   t.splits = (p.kb + t.kb_per_split - 1) / t.kb_per_split;
   t.total = (int)tiles * t.splits;
   const int grid = 2 * (t.total < pairs ? t.total : pairs);

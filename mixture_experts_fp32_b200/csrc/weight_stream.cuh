@@ -69,6 +69,9 @@ struct WsSmem {
 // Tensor map of a row-major matrix [rows, row_bytes] in boxes of box_rows x 128 bytes with
 // the 128-byte swizzle; what lies past its end reads as zero.
 bool ws_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64_t rows, int box_rows);
+// Any tensor of bytes: `rank` extents, the strides of all but the first, and the box.
+bool ws_map_nd(CUtensorMap* m, const void* w, int rank, const uint64_t* dims,
+               const uint64_t* strides, const uint32_t* box);
 
 #if defined(__CUDACC__)
 
@@ -105,6 +108,23 @@ struct WsSplit {
 template <int ROWS>
 __device__ __forceinline__ float* ws_partial(float* part, int b, int first) {
   return part + (size_t)(b * 2 + (b == first ? 1 : 0)) * (ROWS * kWsRows);
+}
+
+// One lane of a warp in step, chosen by the hardware.  Instructions of the tensor core and the
+// TMA take their operands from registers that a warp's lanes share; issued under this vote, in
+// code that the whole warp runs, they find them there.  Under a comparison of the thread's
+// index every operand is carried over first: 100 clocks an instruction, so that four MMAs and
+// their commits (512 clocks of work) took 880.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// The warp's index, as a value that its lanes share.
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
 }
 
 // Bounded wait taken by a whole warp (warp-uniform result): a limit of 0 gives up at once
@@ -196,8 +216,8 @@ struct WsWeights {
   __device__ WsWeights(S& s_, const WsRole& r) : s(s_), role(r) {}
   __device__ __forceinline__ void load(const CUtensorMap* m, int row0, int row1, int koff) {
     if (!role.wait(&s.empty[pos.i], pos.phase ^ 1u)) return;
-    if ((threadIdx.x & 31) == 0) {
-      const uint32_t bar = smem_u32(&s.full_w[pos.i]), dst = smem_u32(s.w[pos.i]);
+    const uint32_t bar = smem_u32(&s.full_w[pos.i]), dst = smem_u32(s.w[pos.i]);
+    if (elect_one()) {
       mbar_arrive_expect_tx(bar, row1 >= 0 ? kWsStageBytes : kWsStageBytes / 2);
       tma_load_2d(dst, m, koff, row0, bar, policy);
       if (row1 >= 0) tma_load_2d(dst + kWsStageBytes / 2, m, koff, row1, bar, policy);
@@ -239,8 +259,8 @@ struct WsActivations {
       slot = (slot + 1) % kWsSlots;
       __syncwarp();
     }
-    if (lane == 0) {
-      const uint32_t bar = smem_u32(&s.full_x[pos.i]);
+    const uint32_t bar = smem_u32(&s.full_x[pos.i]);
+    if (elect_one()) {
       mbar_arrive_expect_tx(bar, box_rows * kWsBytes);
       tma_load_2d(smem_u32(s.x[pos.i]), m, koff, row, bar, policy);
     }
@@ -289,43 +309,47 @@ __device__ __forceinline__ void ws_each_unit_ahead(int tiles, int per, G&& fetch
   }
 }
 
-// MMA issuer (one warp in step, one lane issues): stages from `begin` to `end` share a buffer.
+// MMA issuer (one warp): stages from `begin` to `end` share a buffer.
 template <bool FP8, class S>
 struct WsMma {
   S& s;
   WsRole role;
   WsPos pos, d;
+  uint32_t tmem;
   bool any = false;
-  __device__ WsMma(S& s_, const WsRole& r) : s(s_), role(r) {}
+  __device__ WsMma(S& s_, const WsRole& r)
+      : s(s_), role(r), tmem(__shfl_sync(0xffffffffu, s_.tmem, 0)) {}
   __device__ __forceinline__ void stage(bool begin, bool end) {
     role.wait(&s.full_w[pos.i], pos.phase);
     role.wait(&s.full_x[pos.i], pos.phase);
     if (begin) role.wait(&s.dempty[d.i], d.phase ^ 1u);
     if (!role.ok) return;
     tc_fence_after();
-    if ((threadIdx.x & 31) == 0) {
-      const uint32_t dst = s.tmem + d.i * kWsRows;
-      const uint64_t a = smem_desc_sw128(smem_u32(s.x[pos.i]));
-      const uint64_t b = smem_desc_sw128(smem_u32(s.w[pos.i]));
+    const uint32_t dst = tmem + d.i * kWsRows;
+    const uint64_t a = smem_desc_sw128(smem_u32(s.x[pos.i]));
+    const uint64_t b = smem_desc_sw128(smem_u32(s.w[pos.i]));
+    const uint32_t empty = smem_u32(&s.empty[pos.i]), full = smem_u32(&s.dfull[d.i]);
+    const uint32_t more = begin ? 0u : 1u;
+    if (elect_one()) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {           // 32 bytes of K an instruction
         if (FP8)
-          umma_e4m3(dst, a + 2 * k, b + 2 * k, idesc_e4m3_m128(kWsRows), k > 0 || !begin);
+          umma_e4m3(dst, a + 2 * k, b + 2 * k, idesc_e4m3_m128(kWsRows), k > 0 ? 1u : more);
         else
-          umma_bf16(dst, a + 2 * k, b + 2 * k, idesc_bf16_m128(kWsRows), k > 0 || !begin);
+          umma_bf16(dst, a + 2 * k, b + 2 * k, idesc_bf16_m128(kWsRows), k > 0 ? 1u : more);
       }
-      umma_commit(smem_u32(&s.empty[pos.i]));
-      if (end) umma_commit(smem_u32(&s.dfull[d.i]));
+      umma_commit(empty);
+      if (end) umma_commit(full);
     }
+    __syncwarp();
     if (end) d.next(2);
     any = true;
     pos.next(S::STAGES);
-    __syncwarp();
   }
   // the tensor core has finished before tensor memory is freed
   __device__ __forceinline__ void drain() {
     if (!any) return;
-    if ((threadIdx.x & 31) == 0) umma_commit(smem_u32(&s.teardown));
+    if (elect_one()) umma_commit(smem_u32(&s.teardown));
     __syncwarp();
     ws_wait(smem_u32(&s.teardown), 0, kWsDrainNs, role.status, role.bit);
   }
