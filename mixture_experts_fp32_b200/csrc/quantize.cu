@@ -5,6 +5,15 @@
 // fraction, so everything before the code is fp32.  Bound by HBM: one read of the values,
 // one write of the codes.  Eight lanes take a group, 16 consecutive values a lane: 16-byte
 // loads, and one 16-byte store of codes a lane.
+//
+// The quotients have to be the correctly rounded ones (bf16 values often fall on the border of
+// two codes), but sixteen divisions a lane cost more than the bytes.  They take one
+// reciprocal a lane and four fused multiply-adds a value instead (quotient below), two values
+// an instruction; the next group's loads are on their way meanwhile.  Instructions still bound
+// it more than bytes (7168 columns of 8192 rows of bf16: 40 us, 4400 GB/s; one group at a time
+// with divisions 51 us).  Gated values take more registers than let four blocks share an SM:
+// held to 64 they spill a little and are faster for it (fp32, 4099 rows of 2 x 2064, 900 of them
+// padding: 19 against 21 us).
 #include "moe_internal.cuh"
 
 #define MOE_EXPORT extern "C" __attribute__((visibility("default")))
@@ -14,86 +23,173 @@ namespace {
 
 constexpr int kVals = 16;            // values of a lane
 
-__device__ __forceinline__ void load_vals(const __nv_bfloat16* p, float (&v)[kVals]) {
+// A lane's values as they lie in memory, and as fp32.
+template <typename XT>
+struct Raw {
+  static constexpr int N = kVals * sizeof(XT) / 16;
+  uint4 w[N];
+  __device__ __forceinline__ void load(const XT* p) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint4 r = reinterpret_cast<const uint4*>(p)[h];
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[8 * h + 2 * i] = __uint_as_float(w[i] << 16);
-      v[8 * h + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < N; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void values(float2 (&v)[kVals / 2]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t r[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      if (sizeof(XT) == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[4 * i + j] =
+              make_float2(__uint_as_float(r[j] << 16), __uint_as_float(r[j] & 0xffff0000u));
+      } else {
+        v[2 * i] = make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
+        v[2 * i + 1] = make_float2(__uint_as_float(r[2]), __uint_as_float(r[3]));
+      }
     }
   }
-}
-__device__ __forceinline__ void load_vals(const float* p, float (&v)[kVals]) {
+  // the largest |value| but NaN, of bf16 two at a time
+  __device__ __forceinline__ float amax() const {
+    if (sizeof(XT) == 2) {
+      __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const float4 r = reinterpret_cast<const float4*>(p)[h];
-    v[4 * h] = r.x;
-    v[4 * h + 1] = r.y;
-    v[4 * h + 2] = r.z;
-    v[4 * h + 3] = r.w;
+      for (int i = 0; i < N; ++i) {
+        const uint32_t r[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a = r[j] & 0x7fff7fffu;
+          m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&a));
+        }
+      }
+      return fmaxf(__low2float(m), __high2float(m));
+    }
+    float2 v[kVals / 2];
+    values(v);
+    return largest(v);
   }
+  static __device__ __forceinline__ float largest(const float2 (&v)[kVals / 2]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVals / 2; ++i) m = fmaxf(m, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+    return m;
+  }
+};
+
+// RN(v / s) from r = RN(1 / s) by Markstein's method: a quotient within an ulp (the first
+// correction makes it so) plus r times its exact remainder rounds to the correctly rounded
+// quotient.  For s in [2^-70, 2^100] and |v| <= 448 s: no step then overflows, and none
+// underflows for a quotient that has a code other than 0.
+// (Two values an instruction.)
+__device__ __forceinline__ float2 quotient(float2 v, float s, float r) {
+  const float2 r2 = make_float2(r, r), n2 = make_float2(-s, -s);
+  const float2 q0 = __fmul2_rn(v, r2);
+  const float2 q1 = __ffma2_rn(__ffma2_rn(q0, n2, v), r2, q0);
+  return __ffma2_rn(__ffma2_rn(q1, n2, v), r2, q1);
 }
 
-template <typename XT, bool GATED>
-__global__ void __launch_bounds__(256) quantize_groups_kernel(
+// silu(g) * u; the quotient of silu by the same method (d = 1 + e^-g >= 1; above 2^100 the
+// division itself).
+__device__ __forceinline__ float gated_value(float g, float u) {
+  const float d = 1.0f + expf(-g);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  const float q = g * r;
+  return (d <= 0x1p100f ? fmaf(fmaf(-q, d, g), r, q) : g / d) * u;
+}
+
+// IT: type of the group index (int where rows * groups allows it)
+template <typename XT, bool GATED, typename IT>
+__global__ void __launch_bounds__(256, GATED ? 4 : 3) quantize_groups_kernel(
     const XT* __restrict__ x, const uint8_t* __restrict__ valid, int rows, int cols, long long ldx,
     uint8_t* __restrict__ codes, float* __restrict__ scales) {
   const int groups = (cols + 127) / 128;
   const int sub = threadIdx.x & 7;
-  const long long total = (long long)rows * groups;
-  const long long step = (long long)gridDim.x * (blockDim.x / 8);
+  const IT total = (IT)rows * groups;
+  const IT step = (IT)gridDim.x * (blockDim.x / 8);
   // all lanes of a warp stay in the loop together (the shuffles below)
-  const long long rounds = (total + step - 1) / step;
-  long long u = (long long)blockIdx.x * (blockDim.x / 8) + (threadIdx.x >> 3);
-  for (long long it = 0; it < rounds; ++it, u += step) {
-    const bool in = u < total;
-    const int row = in ? (int)(u / groups) : 0, kb = in ? (int)(u - (long long)row * groups) : 0;
+  const IT rounds = (total + step - 1) / step;
+  IT u = (IT)blockIdx.x * (blockDim.x / 8) + (threadIdx.x >> 3);
+  // the next group's values are under way while this one's are worked on
+  Raw<XT> raw, raw_up;
+  int row, kb;
+  bool mine;
+  auto fetch = [&](IT g) {
+    const bool in = g < total;
+    row = in ? (int)(g / groups) : 0;
+    kb = in ? (int)(g - (IT)row * groups) : 0;
     const int col = kb * 128 + sub * kVals;
-    const bool mine = in && col < cols;
-    float v[kVals];
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) v[i] = 0.f;
+    mine = in && col < cols;
+    raw.clear();
+    if (GATED) raw_up.clear();
     if (mine && (valid == nullptr || valid[row])) {
-      load_vals(x + row * ldx + col, v);
-      if (GATED) {
-        float up[kVals];
-        load_vals(x + row * ldx + cols + col, up);
-#pragma unroll
-        for (int i = 0; i < kVals; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * up[i];
-      }
+      const XT* src = x + row * ldx + col;
+      raw.load(src);
+      if (GATED) raw_up.load(src + cols);
     }
-    float amax = 0.f;
+  };
+  fetch(u);
+  for (IT it = 0; it < rounds; ++it, u += step) {
+    float2 v[kVals / 2];
+    raw.values(v);
+    float amax;
+    if (GATED) {
+      float2 up[kVals / 2];
+      raw_up.values(up);
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) amax = fmaxf(amax, fabsf(v[i]));
+      for (int i = 0; i < kVals / 2; ++i)
+        v[i] = make_float2(gated_value(v[i].x, up[i].x), gated_value(v[i].y, up[i].y));
+      amax = Raw<XT>::largest(v);
+    } else {
+      amax = raw.amax();
+    }
+    const size_t at = (size_t)row * cols + kb * 128 + sub * kVals;
+    const size_t at_scale = (size_t)row * groups + kb;
+    const bool store = mine;
+    if (it + 1 < rounds) fetch(u + step);
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1)
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
     const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-    if (!mine) continue;
+    if (sc >= 0x1p-70f && sc <= 0x1p100f) {
+      const float r = __frcp_rn(sc);
+#pragma unroll
+      for (int i = 0; i < kVals / 2; ++i) v[i] = quotient(v[i], sc, r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVals / 2; ++i)
+        v[i] = make_float2(__fdiv_rn(v[i].x, sc), __fdiv_rn(v[i].y, sc));
+    }
     uint32_t o[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w)
-      o[w] = e4m3_codes4(__fdiv_rn(v[4 * w], sc), __fdiv_rn(v[4 * w + 1], sc),
-                         __fdiv_rn(v[4 * w + 2], sc), __fdiv_rn(v[4 * w + 3], sc));
-    *reinterpret_cast<uint4*>(codes + (size_t)row * cols + col) = make_uint4(o[0], o[1], o[2], o[3]);
-    if (sub == 0) scales[(size_t)row * groups + kb] = sc;
+      o[w] = e4m3_codes4(v[2 * w].x, v[2 * w].y, v[2 * w + 1].x, v[2 * w + 1].y);
+    if (store) {
+      *reinterpret_cast<uint4*>(codes + at) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (sub == 0) scales[at_scale] = sc;
+    }
   }
 }
 
 template <typename XT>
 cudaError_t launch(const void* x, const uint8_t* valid, int rows, int cols, long long ldx,
                    bool gated, void* codes, float* scales, cudaStream_t st) {
-  const long long blocks = ((long long)rows * ((cols + 127) / 128) + 31) / 32;
-  const int grid = (int)(blocks < 148 * 16 ? blocks : 148 * 16);
+  const long long total = (long long)rows * ((cols + 127) / 128), blocks = (total + 31) / 32;
+  const int grid = (int)(blocks < 148 * 8 ? blocks : 148 * 8);
   auto* xt = static_cast<const XT*>(x);
   auto* c = static_cast<uint8_t*>(codes);
+  const auto run = [&](auto kernel) {
+    kernel<<<grid, 256, 0, st>>>(xt, valid, rows, cols, ldx, c, scales);
+  };
+  const bool narrow = total < (1ll << 30);
   if (gated)
-    quantize_groups_kernel<XT, true><<<grid, 256, 0, st>>>(xt, valid, rows, cols, ldx, c, scales);
+    narrow ? run(quantize_groups_kernel<XT, true, int>)
+           : run(quantize_groups_kernel<XT, true, long long>);
   else
-    quantize_groups_kernel<XT, false><<<grid, 256, 0, st>>>(xt, valid, rows, cols, ldx, c, scales);
+    narrow ? run(quantize_groups_kernel<XT, false, int>)
+           : run(quantize_groups_kernel<XT, false, long long>);
   return cudaGetLastError();
 }
 
