@@ -82,6 +82,7 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
   const int kb_h = p.H / 128, kb_i = p.imax / 128;
   const WsRole role{p.wait_limit_ns, p.status, p.timeout_bit};
   WsPromoter<S> sum(s.ws, role);
+  float* const down_parts = p.part + (size_t)2 * kWsCtas * p.T * kWsRows;
 
   // all CTAs meet; what they stored before is visible after
   auto grid_sync = [&](unsigned int* counter) {
@@ -167,8 +168,9 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
     } else if (lane == 0) {
       mbar_arrive(smem_u32(&s.scored));
     }
-    // counters of phases 2 and 3
-    if (tid < 3) p.split_count[tid * kFewMaxCtas + cta] = 0;
+    // partial tiles of gate/up: of the shared expert, of the routed ones
+    if (p.S) ws_clear_partial(ws_partial(p.part, p.T, cta, false), p.T);
+    ws_clear_partial(ws_partial(p.part, p.T, cta, true), p.T);
     if (FP8) {
       // x per 1x128 group, a warp a group: codes of x / s, s = amax / 448
       for (int i = cta * kWsWorkers + warp; i < p.T * kb_h; i += ctas * kWsWorkers) {
@@ -285,6 +287,8 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
     if (tid < p.T && s.ids[tid][0] >= 0) s.pick[kShared][tid] = 0;
     ws_workers_sync();
     if (tid == 0) mbar_arrive(smem_u32(&s.routed));
+    ws_clear_partial(ws_partial(down_parts, p.T, cta, false), p.T);
+    ws_clear_partial(ws_partial(down_parts, p.T, cta, true), p.T);
   }
 
   auto on = [&](int slot, int t) { return t < p.T && s.pick[slot][t] >= 0; };
@@ -296,7 +300,7 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
   const int t_lane = lane & (kTokens - 1);            // a promoter lane's token
 
   // ---- 2b. gate/up: columns 0 .. 127 of a tile are gate values, 128 .. 255 up values
-  auto gate_up = [&](bool routed, int I, int experts, unsigned int* split_count, float* parts) {
+  auto gate_up = [&](bool routed, int I, int experts, float* parts) {
     const int ft = I / 128;
     const WsSplit split(experts * ft, ch_h, ctas);
     const int u1 = split.begin(cta + 1);
@@ -316,18 +320,18 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
       if (promoter) sum.park(kTokens);
       ws_tile_ready();
       if (!worker) continue;
-      int b0 = 0, b1 = 0;
-      if (c1 - c0 < ch_h) {
-        b0 = split.owner(t0);
-        b1 = split.owner(t0 + ch_h - 1);
-        ws_store_partial<kTokens>(s.ws.tile, parts, cta, b0, p.T);
-        if (!ws_arrive_last(split_count + b0, b1 - b0 + 1, &s.flag, false)) continue;
+      // the first of its CTAs finishes a shared tile
+      const WsShare share(split, t0, ch_h);
+      if (cta != share.b0) {
+        ws_store_partial(s.ws.tile, ws_partial(parts, p.T, cta, false), p.T);
+        continue;
       }
       const bool mine = on(slot, t_mine);
       float g[8] = {}, up[8] = {};
       if (mine) {
-        ws_tile_values<kTokens>(s.ws.tile[t_mine], parts, b0, b1, t_mine, 8 * part_mine, g);
-        ws_tile_values<kTokens>(s.ws.tile[t_mine], parts, b0, b1, t_mine, 128 + 8 * part_mine, up);
+        ws_tile_values(s.ws.tile[t_mine], parts, p.T, share, t_mine, 8 * part_mine, sum.role, g);
+        ws_tile_values(s.ws.tile[t_mine], parts, p.T, share, t_mine, 128 + 8 * part_mine, sum.role,
+                       up);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = g[i] / (1.0f + expf(-g[i])) * up[i];
@@ -373,8 +377,8 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
 #pragma unroll
       for (int i = 0; i < kMaxExperts / 32; ++i) A += __popc(s.bitmap[i]);
     }
-    gate_up(routed, routed ? p.I : p.Is, routed ? A : p.S, p.split_count + routed * kFewMaxCtas,
-            p.part + (size_t)routed * kFewMaxCtas * 2 * kTokens * kWsRows);
+    gate_up(routed, routed ? p.I : p.Is, routed ? A : p.S,
+            ws_partial(p.part, p.T, 0, routed));
   }
   if (worker) {
     fence_proxy_async();                              // h is read by TMA
@@ -423,25 +427,22 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
     if (promoter) sum.park(kTokens);
     ws_tile_ready();
     if (!worker) continue;
-    int b0 = 0, b1 = 0;
-    if (c1 - c0 < per) {
-      b0 = split.owner(t0);
-      b1 = split.owner(t0 + per - 1);
-      ws_store_partial<kTokens>(s.ws.tile, p.part, cta, b0, p.T);
-      if (!ws_arrive_last(p.split_count + 2 * kFewMaxCtas + b0, b1 - b0 + 1, &s.flag, false))
-        continue;
-    }
-    const int col = 16 * part_mine;
-    if (t_mine < p.T && tile * kWsRows + col < p.H) {
-      float v[16];
-      ws_tile_values<kTokens>(s.ws.tile[t_mine], p.part, b0, b1, t_mine, col, v);
-      const bool real = s.ids[t_mine][0] >= 0;
-      uint32_t o[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = real ? two_bf16(v[2 * i], v[2 * i + 1]) : 0u;
-      uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)t_mine * p.H + tile * kWsRows + col);
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    const WsShare share(split, t0, per);
+    const int n = share.finishers();
+    if (share.b0 != share.b1 && (cta == share.b1 || n > 1))
+      ws_store_partial(s.ws.tile, ws_partial(down_parts, p.T, cta, cta == share.b0), p.T);
+    if (share.b0 != share.b1 && cta == share.b1) continue;
+    // an n-th of the columns, four a thread
+    const int q0 = (kWsRows / 4) * (cta - share.b0) / n, q1 = (kWsRows / 4) * (cta - share.b0 + 1) / n;
+#pragma unroll 1
+    for (int i = tid; i < p.T * (q1 - q0); i += kWsThreads) {
+      const int t = i / (q1 - q0), col = 4 * (q0 + i - t * (q1 - q0));
+      if (tile * kWsRows + col >= p.H) continue;
+      float v[4];
+      ws_tile_values(s.ws.tile[t], down_parts, p.T, share, t, col, sum.role, v);
+      const bool real = s.ids[t][0] >= 0;
+      *reinterpret_cast<uint2*>(p.out + (size_t)t * p.H + tile * kWsRows + col) =
+          make_uint2(real ? two_bf16(v[0], v[1]) : 0u, real ? two_bf16(v[2], v[3]) : 0u);
     }
   }
 }
@@ -665,7 +666,7 @@ cudaError_t prepare_few_kernels() {
 }
 
 cudaError_t launch_few(FewArgs a, bool fp8, int num_sms, cudaStream_t st) {
-  const int ctas = num_sms < kFewMaxCtas ? num_sms : kFewMaxCtas;
+  const int ctas = num_sms < kWsCtas ? num_sms : kWsCtas;
   // eight experts a CTA; with CTAs left over K is cut too, a chunk of 32 a warp at least
   const int groups = (a.E + 7) / 8;
   const int most = a.H / 32 / kWsWorkers < kFewRouterSplits ? a.H / 32 / kWsWorkers : kFewRouterSplits;

@@ -22,7 +22,7 @@ struct moe_plan_s {
       off_ids, off_w, off_perm,
       off_inv, off_rowtok, off_xp, off_sx, off_h, off_sh, off_y;
   // moe_forward_few
-  size_t off_few_logits, off_few_counters, off_few_part, off_few_h, off_few_sh;
+  size_t off_few_logits, off_few_part, off_few_h, off_few_sh;
   int few_slots;
   unsigned long long wait_limit_ns;
   int device;
@@ -210,9 +210,8 @@ MOE_EXPORT moe_status moe_plan_create(const moe_config* cfg, moe_plan_t* plan,
   p->few_slots = (int)slots;
   p->off_few_logits =
       take(sizeof(float) * moe::kFewRouterSplits * MOE_FEW_TOKENS_MAX * E);
-  p->off_few_counters = take(sizeof(unsigned int) * 3 * moe::kFewMaxCtas);
   p->off_few_part =
-      take(sizeof(float) * moe::kFewMaxCtas * 4 * MOE_FEW_TOKENS_MAX * moe::kWsRows);
+      take(sizeof(float) * moe::kWsCtas * 4 * MOE_FEW_TOKENS_MAX * moe::kWsRows);
   const bool few_fp8 = c.wtype != MOE_W_BF16;
   p->off_few_h = take(few_rows * (size_t)imax * (few_fp8 ? 1 : 4));
   p->off_few_sh = few_fp8 ? take(sizeof(float) * few_rows * (imax / 128)) : 0;
@@ -560,7 +559,6 @@ MOE_EXPORT moe_status moe_forward_few(moe_plan_t plan, const moe_weights* wts, c
   a.xq = at<uint8_t>(workspace, plan->off_xp);
   a.sx = at<float>(workspace, plan->off_sx);
   a.part = at<float>(workspace, plan->off_few_part);
-  a.split_count = at<unsigned int>(workspace, plan->off_few_counters);
   a.status = at<unsigned int>(workspace, plan->off_status);
   a.bar = a.status + 16;               // beside the status word, cleared with it
   a.timeout_bit = MOE_DEV_WAIT_TIMEOUT_FEW;

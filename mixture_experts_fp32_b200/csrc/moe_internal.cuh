@@ -159,8 +159,8 @@ cudaError_t prepare_grouped_gemm_kernels();
 
 // The few-token layer (few.cu).
 constexpr int kFewSlots = MOE_FEW_TOKENS_MAX * kMaxTopK;   // distinct experts, at most
-constexpr int kFewMaxCtas = 160;
 constexpr int kFewRouterSplits = 16;
+constexpr int kWsCtas = 160;                               // of a weight stream, at most
 struct FewArgs {
   const __nv_bfloat16* x;
   const uint8_t* valid;
@@ -177,8 +177,7 @@ struct FewArgs {
   float* sh;                     // FP8: scales of h
   uint8_t* xq;                   // FP8: codes and scales of x
   float* sx;
-  float* part;                   // partial tiles [2 ranges][CTA][head, tail]
-  unsigned int* split_count;     // [3 ranges][kFewMaxCtas], zeroed by the kernel
+  float* part;                   // partial tiles [gate/up: shared, routed; down: head, tail][CTA]
   unsigned int* bar;             // two grid barriers, zero before the launch
   unsigned int* status;
   unsigned int timeout_bit;

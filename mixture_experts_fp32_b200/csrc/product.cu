@@ -51,7 +51,6 @@ __device__ __forceinline__ void store_out4(const ProductArgs& p, int m, int n, c
 template <int ROWS>
 struct RowsSmem {
   WsSmem<ROWS, ROWS, ROWS == 16 ? 6 : 5> ws;          // as many stages as 227 KB hold
-  int flag;
 };
 
 template <int ROWS>
@@ -112,19 +111,20 @@ __global__ void __launch_bounds__(kWsBlock, 1)
       if (promoter) sum.park(ROWS);
       ws_tile_ready();
       if (!worker) continue;
-      int b0 = 0, b1 = 0;
-      if (c1 - c0 < per) {
-        b0 = split.owner(t0);
-        b1 = split.owner(t0 + per - 1);
-        ws_store_partial<ROWS>(s.ws.tile, p.part, cta, b0, p.M);
-        if (!ws_arrive_last(p.counters + b0, b1 - b0 + 1, &s.flag, true)) continue;
-      }
-      // four columns of a row a thread at a time
-      for (int i = tid; i < p.M * (kWsRows / 4); i += kWsThreads) {
-        const int m = i / (kWsRows / 4), col = i % (kWsRows / 4) * 4, n = tile * kWsRows + col;
+      const WsShare share(split, t0, per);
+      const int parts = share.finishers();
+      if (share.b0 != share.b1 && (cta == share.b1 || parts > 1))
+        ws_store_partial(s.ws.tile, ws_partial(p.part, p.M, cta, cta == share.b0), p.M);
+      if (share.b0 != share.b1 && cta == share.b1) continue;
+      // a part of the columns, four of a row a thread at a time
+      const int mine = cta - share.b0, q0 = (kWsRows / 4) * mine / parts,
+                q = (kWsRows / 4) * (mine + 1) / parts - q0;
+#pragma unroll 1
+      for (int i = tid; i < p.M * q; i += kWsThreads) {
+        const int m = i / q, col = 4 * (q0 + i - m * q), n = tile * kWsRows + col;
         if (n >= p.N) continue;
         float v[4];
-        ws_tile_values<ROWS>(s.ws.tile[m], p.part, b0, b1, m, col, v);
+        ws_tile_values(s.ws.tile[m], p.part, p.M, share, m, col, sum.role, v);
         store_out4(p, m, n, v);
       }
     }
@@ -137,8 +137,24 @@ cudaError_t launch_rows(const ProductArgs& a, int ctas, cudaStream_t st) {
   CUtensorMap am, wm;
   if (!ws_map(&am, a.a, a.K, a.M, ROWS) || !ws_map(&wm, a.w, a.K, a.N, kWsBoxRows))
     return cudaErrorInvalidValue;
-  product_rows_kernel<ROWS><<<ctas, kWsBlock, sizeof(RowsSmem<ROWS>) + 1024, st>>>(wm, am, a);
-  return cudaGetLastError();
+  // the status word and, where tiles are shared, the partial tiles: heads, and tails if a tile
+  // has more than two CTAs
+  const WsSplit split((a.N + kWsRows - 1) / kWsRows, a.kb, ctas);
+  const int slots = split.whole(a.kb) ? 0 : split.each >= a.kb ? kWsCtas : 2 * kWsCtas;
+  const cudaError_t e = cudaMemsetAsync(
+      a.status, 0, product_head_bytes(a) + sizeof(float) * slots * a.M * kWsRows, st);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kWsBlock, 1, 1);
+  cfg.dynamicSmemBytes = sizeof(RowsSmem<ROWS>) + 1024;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];                        // the CTAs wait for one another
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, product_rows_kernel<ROWS>, wm, am, a);
 }
 
 template <int ROWS>
@@ -175,7 +191,7 @@ MOE_EXPORT moe_status moe_product_create(const moe_product_config* cfg, moe_prod
   p->off_part = 256 + 1024;
   static_assert(sizeof(unsigned int) * moe::kProductCounters <= 1024, "");
   // partial tiles: two a CTA of the weight stream, one a cluster pair of the tiles
-  const size_t stream = sizeof(float) * 2 * moe::kProductCtas * moe::kWsRows *
+  const size_t stream = sizeof(float) * 2 * moe::kWsCtas * moe::kWsRows *
                         (size_t)(cfg->max_rows <= 16 ? 16 : moe::kProductRows);
   const size_t tiles = sizeof(float) * moe::kProductPairs * 256 * 256;
   p->ws_bytes = p->off_part + (cfg->max_rows > moe::kProductRows && tiles > stream ? tiles : stream);
@@ -213,8 +229,6 @@ MOE_EXPORT moe_status moe_block_scaled_product(moe_product_t p, const void* a,
   if (s != MOE_OK) return s;
   auto* st = static_cast<cudaStream_t>(stream);
   auto* ws = static_cast<uint8_t*>(workspace);
-  // the status word and the counters
-  if ((s = moe::cuda_status(cudaMemsetAsync(ws, 0, p->off_part, st))) != MOE_OK) return s;
   moe::ProductArgs g;
   memset(&g, 0, sizeof(g));
   g.w = static_cast<const uint8_t*>(w);
@@ -232,7 +246,7 @@ MOE_EXPORT moe_status moe_block_scaled_product(moe_product_t p, const void* a,
   g.sa = a_scales;
   g.out = out;
   g.M = rows;
-  const int ctas = sms < moe::kProductCtas ? sms : moe::kProductCtas;
+  const int ctas = sms < moe::kWsCtas ? sms : moe::kWsCtas;
   return moe::cuda_status(rows > moe::kProductRows ? moe::launch_product_tiles(g, sms, st)
                           : rows > 16             ? moe::launch_rows<32>(g, ctas, st)
                                                   : moe::launch_rows<16>(g, ctas, st));

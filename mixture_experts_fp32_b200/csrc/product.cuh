@@ -7,11 +7,8 @@
 namespace moe {
 
 constexpr int kProductRows = 32;               // rows the weight stream takes
-constexpr int kProductCtas = 160;
 constexpr int kProductPairs = 80;
-// counters: of shared tiles of the weight stream, or of the tiles' two halves
-constexpr int kProductCounters = 160;
-static_assert(kProductCounters >= kProductCtas && kProductCounters >= 2 * kProductPairs, "");
+constexpr int kProductCounters = 2 * kProductPairs;   // of the tiles' two halves
 
 struct ProductArgs {
   const uint8_t* a;
@@ -27,6 +24,11 @@ struct ProductArgs {
   unsigned int* status;
   unsigned long long wait_limit_ns;
 };
+
+// What lies before the partial sums: status word and counters.
+inline size_t product_head_bytes(const ProductArgs& p) {
+  return reinterpret_cast<uint8_t*>(p.part) - reinterpret_cast<uint8_t*>(p.status);
+}
 
 cudaError_t launch_product_tiles(const ProductArgs& p, int num_sms, cudaStream_t st);
 cudaError_t prepare_product_tiles();

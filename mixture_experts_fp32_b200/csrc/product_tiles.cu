@@ -614,6 +614,8 @@ cudaError_t launch_product_tiles(const ProductArgs& p, int num_sms, cudaStream_t
   t.splits = (p.kb + t.kb_per_split - 1) / t.kb_per_split;
   t.total = (int)tiles * t.splits;
   const int grid = 2 * (t.total < pairs ? t.total : pairs);
+  const cudaError_t e = cudaMemsetAsync(p.status, 0, product_head_bytes(p), st);
+  if (e != cudaSuccess) return e;
   if (p.f32)
     product_tiles_kernel<true><<<grid, kThreads, sizeof(TileSmem) + 1024, st>>>(ma, mw, t);
   else

@@ -22,9 +22,15 @@
 //    buffer takes a whole run of K.
 //
 // Work is cut into units of one stage.  Each CTA takes a contiguous range of the units
-// (within one unit of an even split, whatever the shapes); a tile whose units fall to
-// several CTAs is finished by the last of them to arrive, which adds the partial tiles
-// from global memory in CTA order, so results do not depend on timing.
+// (within one unit of an even split, whatever the shapes).  A tile whose units fall to
+// several CTAs meets in global memory: each stores its partial sums where zeros lay, and
+// who finishes a part of the tile reads them until none is zero, so a value announces
+// itself (a sum of +0 travels as -0, which adds the same).  No counter, no fence, no order of
+// arrival: one trip to L2.  (Counters with the last to arrive finishing took 8000 clocks
+// and more beside a full ring of loads.)  The CTAs in whose range the tile comes last share
+// the finishing; the last of its CTAs, which has it first, has long gone on by then.  Sums
+// are added in a fixed order, so results do not depend on timing.  The CTAs wait for one
+// another: cooperative launches.
 //
 // Fifteen warps: 1 weight producer, 2 MMA issuer, 3 activation producer; promoters 0, 4, 8, 12
 // (lane: activation row; warp / 4: columns, i.e. weight rows, 64 (warp / 4) .. + 63); the
@@ -82,16 +88,20 @@ bool ws_map_nd(CUtensorMap* m, const void* w, int rank, const uint64_t* dims,
 constexpr int kWsLeast = 3;
 struct WsSplit {
   int each, more;
-  __device__ __forceinline__ WsSplit(int tiles, int per, int ctas) {
+  __host__ __device__ __forceinline__ WsSplit(int tiles, int per, int ctas) {
     const int units = tiles * per;
     if (units < ctas * kWsLeast)
       ctas = tiles < ctas && per <= 2 * kWsLeast ? tiles
-                                                 : max(1, min(ctas, units / kWsLeast));
+                                                 : units / kWsLeast > 0 ? units / kWsLeast : 1;
     each = ctas > 0 ? units / ctas : 0;
     more = units - each * ctas;
     last = ctas;
   }
   int last;                                   // CTAs that take part
+  // no tile has several CTAs
+  __host__ __device__ __forceinline__ bool whole(int per) const {
+    return each % per == 0 && more == 0;
+  }
   __device__ __forceinline__ int begin(int cta) const {
     const int b = min(cta, last);
     return b * each + min(b, more);
@@ -102,12 +112,18 @@ struct WsSplit {
   }
 };
 
-// A tile that several CTAs share: CTA b's partial tile [ROWS][kWsRows].  The first of them
-// ends inside the tile (its tail), the others begin inside it (their head); part: [CTA][head,
-// tail].
-template <int ROWS>
-__device__ __forceinline__ float* ws_partial(float* part, int b, int first) {
-  return part + (size_t)(b * 2 + (b == first ? 1 : 0)) * (ROWS * kWsRows);
+
+// The sharers of the tile that begins at unit t0: CTAs b0 .. b1.
+struct WsShare {
+  int b0, b1;
+  __device__ __forceinline__ WsShare(const WsSplit& split, int t0, int per)
+      : b0(split.owner(t0)), b1(split.owner(t0 + per - 1)) {}
+  __device__ __forceinline__ int finishers() const { return max(b1 - b0, 1); }
+};
+// CTA b's partial tile [rows][kWsRows]: of the tile that its range begins inside of, or (tail)
+// of the one that its range is first to touch.  part: [head, tail][kWsCtas].
+__device__ __forceinline__ float* ws_partial(float* part, int rows, int b, bool tail) {
+  return part + (size_t)((tail ? kWsCtas : 0) + b) * rows * kWsRows;
 }
 
 // One lane of a warp in step, chosen by the hardware.  Instructions of the tensor core and the
@@ -427,66 +443,83 @@ __device__ __forceinline__ unsigned int atomic_add_acq_rel(unsigned int* p) {
   return v;
 }
 
-// Several CTAs share something: true, for all workers, in the CTA that arrives last.  What the
-// others' workers stored before is visible after.
-__device__ __forceinline__ bool ws_arrive_last(unsigned int* counter, unsigned int expected,
-                                               int* flag, bool reset) {
-  ws_workers_sync();
-  if (ws_worker_thread() == 0) {
-    const bool last = atomic_add_acq_rel(counter) + 1 == expected;
-    if (last && reset) *counter = 0;
-    *flag = last;
-  }
-  ws_workers_sync();
-  return *flag != 0;
-}
-
-// The workers' view of a finished tile: value (row, col) and up to V - 1 behind it, from the
-// shared tile or, where several CTAs share the tile, summed over their partial tiles in CTA
-// order.
-template <int ROWS, int V>
-__device__ __forceinline__ void ws_tile_values(const float* tile_row, float* part, int b0, int b1,
-                                               int row, int col, float (&v)[V]) {
-  static_assert(V % 4 == 0, "");
-  if (b0 == b1) {
-#pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      const float4 o = *reinterpret_cast<const float4*>(tile_row + col + 4 * i);
-      v[4 * i] = o.x; v[4 * i + 1] = o.y; v[4 * i + 2] = o.z; v[4 * i + 3] = o.w;
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = 0.f;
-  for (int b = b0; b <= b1; b += 4) {
-    float4 o[4][V / 4];                       // the loads of four CTAs go out together
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i)
-        o[j][i] = b + j <= b1 ? __ldcg(reinterpret_cast<const float4*>(
-                                    ws_partial<ROWS>(part, b + j, b0) + row * kWsRows + col) + i)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        v[4 * i] += o[j][i].x; v[4 * i + 1] += o[j][i].y;
-        v[4 * i + 2] += o[j][i].z; v[4 * i + 3] += o[j][i].w;
-      }
-  }
-}
-
-// This CTA's share of a tile from shared memory to its partial tile.
-template <int ROWS>
-__device__ __forceinline__ void ws_store_partial(const float (*tile)[kWsTilePitch], float* part,
-                                                 int cta, int b0, int rows) {
-  float* o = ws_partial<ROWS>(part, cta, b0);
+// This CTA's share of a tile from shared memory to its (zeroed) partial tile.
+__device__ __forceinline__ void ws_store_partial(const float (*tile)[kWsTilePitch], float* o,
+                                                 int rows) {
+#pragma unroll 1
   for (int i = ws_worker_thread(); i < rows * (kWsRows / 4); i += kWsThreads) {
     const int row = i / (kWsRows / 4), c = i % (kWsRows / 4);
-    reinterpret_cast<float4*>(o + row * kWsRows)[c] =
-        reinterpret_cast<const float4*>(tile[row])[c];
+    float4 v = reinterpret_cast<const float4*>(tile[row])[c];
+    v.x = __float_as_uint(v.x) ? v.x : -0.f;
+    v.y = __float_as_uint(v.y) ? v.y : -0.f;
+    v.z = __float_as_uint(v.z) ? v.z : -0.f;
+    v.w = __float_as_uint(v.w) ? v.w : -0.f;
+    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(
+                     reinterpret_cast<float4*>(o + row * kWsRows) + c),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
   }
+}
+
+// v = value (row, col) and the V - 1 behind it of a finished tile: this CTA's sums from the
+// shared tile and, where several CTAs share it, the others' partial tiles in CTA order, each
+// awaited.
+template <int V>
+__device__ __forceinline__ void ws_tile_values(const float* tile_row, float* part, int rows,
+                                               const WsShare& sh, int row, int col, WsRole& role,
+                                               float (&v)[V]) {
+  static_assert(V % 4 == 0, "");
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    const float4 o = *reinterpret_cast<const float4*>(tile_row + col + 4 * i);
+    v[4 * i] = o.x; v[4 * i + 1] = o.y; v[4 * i + 2] = o.z; v[4 * i + 3] = o.w;
+  }
+  const int me = blockIdx.x;
+  constexpr int kMany = V > 8 ? 1 : 16 / V;           // CTAs whose loads go out together
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (int b = sh.b0; b <= sh.b1; b += kMany) {
+    float o[kMany][V];
+    while (true) {
+      bool there = true;
+#pragma unroll
+      for (int j = 0; j < kMany; ++j) {
+        const bool other = b + j <= sh.b1 && b + j != me;
+        const float* at = ws_partial(part, rows, b + j, b + j == sh.b0) + row * kWsRows + col;
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          o[j][i] = o[j][i + 1] = o[j][i + 2] = o[j][i + 3] = -0.f;
+          if (other)
+            asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(o[j][i]), "=f"(o[j][i + 1]), "=f"(o[j][i + 2]), "=f"(o[j][i + 3])
+                         : "l"(at + i)
+                         : "memory");
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kMany; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) there &= __float_as_uint(o[j][i]) != 0u;
+      if (there || !role.ok) break;
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 >= role.limit_ns) {
+        atomicOr(role.status, role.bit);
+        role.ok = false;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kMany; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] += o[j][i];
+  }
+}
+
+// Zeroes of this CTA's partial tile, by the workers.
+__device__ __forceinline__ void ws_clear_partial(float* o, int rows) {
+#pragma unroll 1
+  for (int i = ws_worker_thread(); i < rows * (kWsRows / 4); i += kWsThreads)
+    __stcg(reinterpret_cast<float4*>(o) + i, make_float4(0.f, 0.f, 0.f, 0.f));
 }
 
 // Generic-proxy stores to global memory before, bulk (async-proxy) loads of them after.
