@@ -40,14 +40,14 @@ constexpr int kTokens = MOE_FEW_TOKENS_MAX;           // rows of every product
 template <bool FP8>
 struct FewSmem {
   static constexpr int kParts = FP8 ? 1 : 2;          // of h
-  WsSmem<kParts * kTokens, kTokens, FP8 ? 6 : 5> ws;
+  WsSmem<FP8, kParts * kTokens, kTokens, FP8 ? 6 : 5> ws;
   float w[kTokens][kMaxTopK];                         // routing weights
   int ids[kTokens][kMaxTopK];                         // routed experts, -1 in padding rows
   short active[kFewSlots];                            // the distinct experts, ascending
   signed char pick[kFewSlots + 1][kTokens];           // j with ids[t][j] = active[slot], or -1
   unsigned int bitmap[kMaxExperts / 32];
-  // router's weights read; x quantised; selection made; h complete
-  uint64_t scored, ready, routed, met;
+  // router's weights read; x quantised; selection made; this CTA's part of h made; h complete
+  uint64_t scored, ready, routed, drained, met;
   int flag;
 };
 
@@ -69,26 +69,190 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The workers' and promoters' part.
+// logits[t * E + e] = the sum of at most SPLITS splits' values, N of them a thread at a time.
+template <int N, int SPLITS>
+__device__ __forceinline__ void sum_logits(const FewArgs& p, int tid, float* logits) {
+  const int n = p.T * p.E;
+#pragma unroll 1
+  for (int i = tid; i < n; i += N * kWsThreads) {
+    float part[N][SPLITS];
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int sp = 0; sp < SPLITS; ++sp)
+        part[j][sp] = sp < p.router_splits && i + j * kWsThreads < n
+                          ? __ldcg(p.logits + (size_t)sp * kTokens * p.E + i + j * kWsThreads)
+                          : 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float l = part[j][0];
+#pragma unroll
+      for (int sp = 1; sp < SPLITS; ++sp) l += part[j][sp];
+      if (i + j * kWsThreads < n) logits[i + j * kWsThreads] = l;
+    }
+  }
+}
+
+// The experts and weights of token t, by a warp; N: experts a lane, E <= 32 N.
+template <int N, bool FP8>
+__device__ __forceinline__ void select(FewSmem<FP8>& s, const FewArgs& p, const float* logits, int t) {
+  const int lane = threadIdx.x & 31, cta = blockIdx.x;
+  const bool real = p.valid == nullptr || p.valid[t];
+  // Logits as keys of their order (larger float, larger key; -0 as +0; at least 1, and 0 once
+  // taken), so that a round is two warp reductions: the largest key, then the lowest expert
+  // that has it.  The rounds are a loop, not unrolled: every launch fetches this code anew,
+  // and it runs once (unrolled, the selection took 11000 clocks for 8 experts, as a loop
+  // 3000).
+  float v[N];
+  uint32_t key[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    v[i] = lane + 32 * i < p.E ? logits[t * p.E + lane + 32 * i] : 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = 0;
+    if (e < p.E) {
+      const uint32_t u = __float_as_uint(v[i] + 0.f);
+      key[i] = max(u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u), 1u);
+      if (cta == 0 && p.logits_out != nullptr)
+        p.logits_out[(size_t)t * p.E + e] = real ? v[i] : 0.f;
+    }
+  }
+  int mine_e = -1;                                  // lane j: the j-th expert and its logit
+  float mine_v = 0.f;
+  if (real) {
+#pragma unroll 1
+    for (int j = 0; j < p.k; ++j) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) best = max(best, key[i]);
+      best = __reduce_max_sync(0xffffffffu, best);
+      int e = kMaxExperts;
+#pragma unroll
+      for (int i = N - 1; i >= 0; --i)
+        if (key[i] == best) e = lane + 32 * i;
+      e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (e == lane + 32 * i) key[i] = 0;
+      if (lane == j) {
+        mine_e = e;
+        mine_v = __uint_as_float(best ^ ((best >> 31) ? 0x80000000u : 0xffffffffu));
+      }
+    }
+  }
+  const float top = __shfl_sync(0xffffffffu, mine_v, 0);
+  const float ex = real && lane < p.k ? expf(mine_v - top) : 0.f;
+  float z = ex;
+  if (!p.renorm) {
+    z = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (lane + 32 * i < p.E) z += expf(v[i] - top);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+  if (lane < p.k) {
+    const float w = real ? ex / z : 0.f;
+    s.ids[t][lane] = mine_e;
+    s.w[t][lane] = w;
+    if (real) atomicOr(&s.bitmap[mine_e >> 5], 1u << (mine_e & 31));
+    if (cta == 0 && p.ids_out != nullptr) p.ids_out[t * p.k + lane] = mine_e;
+    if (cta == 0 && p.w_out != nullptr) p.w_out[t * p.k + lane] = w;
+  }
+}
+
+// A token's place in the tiles of a slot (an expert's, or the shared one's).
 template <bool FP8>
-__device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, int ch_h, int ch_i,
+__device__ __forceinline__ bool few_on(const FewSmem<FP8>& s, const FewArgs& p, int slot, int t) {
+  return t < p.T && s.pick[slot][t] >= 0;
+}
+template <bool FP8>
+__device__ __forceinline__ int few_active(const FewSmem<FP8>& s) {   // distinct experts
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxExperts / 32; ++i) n += __popc(s.bitmap[i]);
+  return n;
+}
+
+// The promoters' part.
+template <bool FP8>
+__device__ __forceinline__ void few_promote(FewSmem<FP8>& s, const FewArgs& p, int ch_h, int ch_i,
                                             int ch_s) {
   using S = decltype(s.ws);
+  const int lane = threadIdx.x & 31, t_lane = lane & (kTokens - 1);
+  WsPromoter<S> sum(s.ws, WsRole{p.wait_limit_ns, p.status, p.timeout_bit});
+  auto done = [&]() {
+    ws_tile_free();
+    sum.park(kTokens);
+    ws_tile_ready();
+  };
+  // at the shared expert while the workers still select the routed ones
+  int A = 0;
+#pragma unroll 1                                      // one copy of the code
+  for (int routed = 0; routed < 2; ++routed) {
+    if (routed) {
+      ws_tile_free();                                 // now the selection is known to both
+      A = few_active(s);
+    }
+    const int tiles = routed ? A * (p.I / 128) : p.S * (p.Is / 128);
+    ws_each_run(WsSplit(tiles, ch_h, gridDim.x), ch_h, [&](int, int c0, int c1, int) {
+      sum.clear();
+      // bf16: one buffer takes the whole run
+      for (int c = FP8 ? c0 : c1 - 1; c < c1; ++c) sum.add(1.f, lane < p.T);
+      done();
+    });
+  }
+  if (A == 0) return;
+  const int per = ch_s + A * ch_i;
+  ws_each_run(WsSplit((p.H + kWsRows - 1) / kWsRows, per, gridDim.x), per,
+              [&](int, int c0, int c1, int) {
+    sum.clear();
+    for (int c = c0; c < c1;) {
+      // the run of stages of one slot
+      const int slot = c < ch_s ? kShared : (c - ch_s) / ch_i;
+      const int first = slot == kShared ? 0 : ch_s + slot * ch_i;
+      const int end = min(c1, first + (slot == kShared ? ch_s : ch_i));
+      // a token that did not select this expert takes nothing from it, not even 0 * inf
+      const bool take = (!FP8 || lane < kTokens) && few_on(s, p, slot, t_lane);
+      const float f = take && slot != kShared ? s.w[t_lane][(int)s.pick[slot][t_lane]] : 1.f;
+      if (FP8) {
+        for (; c < end; ++c) sum.add(f, take);
+      } else {
+        sum.add(f, take);
+        c = end;
+      }
+    }
+    if (!FP8) {                                       // high and low part of h
+#pragma unroll
+      for (int i = 0; i < kWsCols; ++i)
+        sum.acc[i] += __shfl_down_sync(0xffffffffu, sum.acc[i], kTokens);
+    }
+    done();
+  });
+}
+
+// The workers' part.
+template <bool FP8>
+__device__ __forceinline__ void few_work(FewSmem<FP8>& s, const FewArgs& p, int ch_h, int ch_i,
+                                         int ch_s) {
   constexpr int EB = FP8 ? 1 : 2;
   constexpr int kParts = FewSmem<FP8>::kParts;
   const int tid = ws_worker_thread(), warp = tid >> 5, lane = threadIdx.x & 31;
-  const bool worker = tid >= 0, promoter = !worker;
   const int cta = blockIdx.x, ctas = gridDim.x;
   const int kb_h = p.H / 128, kb_i = p.imax / 128;
-  const WsRole role{p.wait_limit_ns, p.status, p.timeout_bit};
-  WsPromoter<S> sum(s.ws, role);
+  WsRole role{p.wait_limit_ns, p.status, p.timeout_bit};
   float* const down_parts = p.part + (size_t)2 * kWsCtas * p.T * kWsRows;
 
-  // all CTAs meet; what they stored before is visible after
-  auto grid_sync = [&](unsigned int* counter) {
+  // All CTAs meet: `arrive`, then `meet`, after which what they stored before is visible.
+  bool met = false;                                   // thread 0's
+  auto arrive = [&](unsigned int* counter) {
     ws_workers_sync();
+    if (tid == 0) met = atomic_add_acq_rel(counter) + 1 >= (unsigned int)ctas;
+  };
+  auto meet = [&](unsigned int* counter) {
     if (tid == 0) {
-      bool met = atomic_add_acq_rel(counter) + 1 >= (unsigned int)ctas;
       const uint64_t t0 = global_timer_ns();
       while (!met) {
         met = ld_acquire_gpu(counter) >= (unsigned int)ctas;
@@ -100,16 +264,26 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
       s.flag = met;
     }
     ws_workers_sync();
-    if (!s.flag) sum.role.ok = false;
+    if (!s.flag) role.ok = false;
   };
 
-  if (worker) {
+  {
     // ---- 1. router logits: eight experts and a part of K a CTA, on m16n8k16 products with the
     // fp32 weights split exactly into three bf16 parts (each the nearest bf16 of what is
     // left), so the sums are the fp32 sums with the full weights.  Few instructions, as for
     // the selection below: every launch fetches this code anew.  (As an unrolled loop of
     // fp32 FMAs, sixteen tokens took 32000 clocks.)
     const int groups = (p.E + 7) / 8, chunks = p.H / 32;
+    // FP8: x per 1x128 group, a warp a group, codes of x / s, s = amax / 448; loaded before the
+    // router's products, which take the first CTAs, and stored after them
+    const auto x_group = [&](int i) {
+      const int t = i / kb_h, kb = i - t * kb_h;
+      return t < p.T ? *reinterpret_cast<const uint2*>(p.x + (size_t)t * p.H + kb * 128 + lane * 4)
+                     : make_uint2(0, 0);
+    };
+    int xi = (ctas - 1 - cta) * kWsWorkers + warp;
+    uint2 xv = make_uint2(0, 0);
+    if (FP8) xv = x_group(xi);
     if (cta < groups * p.router_splits) {
       const int split = cta / groups, e0 = (cta - split * groups) * 8;
       const int g = lane >> 2, q = lane & 3;
@@ -172,11 +346,11 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
     if (p.S) ws_clear_partial(ws_partial(p.part, p.T, cta, false), p.T);
     ws_clear_partial(ws_partial(p.part, p.T, cta, true), p.T);
     if (FP8) {
-      // x per 1x128 group, a warp a group: codes of x / s, s = amax / 448
-      for (int i = cta * kWsWorkers + warp; i < p.T * kb_h; i += ctas * kWsWorkers) {
-        const int t = i / kb_h, kb = i - t * kb_h;
+      for (; xi < p.T * kb_h; xi += ctas * kWsWorkers) {
+        const int t = xi / kb_h, kb = xi - t * kb_h;
+        const uint2 v = xv;
+        xv = x_group(xi + ctas * kWsWorkers);
         if (p.valid != nullptr && !p.valid[t]) continue;
-        const uint2 v = *reinterpret_cast<const uint2*>(p.x + (size_t)t * p.H + kb * 128 + lane * 4);
         const float f[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
                             __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
         float sc;
@@ -186,90 +360,27 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
       }
     }
     if (FP8) fence_proxy_async();                       // the codes are read by TMA
-    grid_sync(p.bar);
+    arrive(p.bar);
+
+    meet(p.bar);
     if (FP8 && tid == 0) mbar_arrive(smem_u32(&s.ready));
 
-    // ---- 2a. the experts of every token, by every CTA for itself
+    // ---- 2a. the experts of every token, by every CTA for itself; first the logits of all
+    // splits, with as many loads on their way as there are (behind the ring's loads each
+    // round trip takes up to 4 us)
+    float* const logits = &s.ws.tile[0][0];
+    if (p.router_splits <= 4)
+      sum_logits<8, 4>(p, tid, logits);
+    else
+      sum_logits<2, kFewRouterSplits>(p, tid, logits);
+    ws_workers_sync();
     for (int t = warp; t < p.T; t += kWsWorkers) {
-      const bool real = p.valid == nullptr || p.valid[t];
-      // Logits as keys of their order (larger float, larger key; -0 as +0; at least 1, and 0 once
-      // taken), so that a round is two warp reductions: the largest key, then the lowest expert
-      // that has it.  The rounds are a loop, not unrolled: every launch fetches this code anew,
-      // and it runs once (unrolled, the selection took 11000 clocks for 8 experts, as a loop
-      // 3000).
-      float v[8];
-      uint32_t key[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-#pragma unroll 1
-      for (int sp = 0; sp < p.router_splits; sp += 4) {
-        float part[4][8];                             // every load before the first use
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            part[j][i] = sp + j < p.router_splits && lane + 32 * i < p.E
-                             ? __ldcg(p.logits + ((size_t)(sp + j) * kTokens + t) * p.E + lane +
-                                      32 * i)
-                             : 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += part[j][i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = lane + 32 * i;
-        key[i] = 0;
-        if (e < p.E) {
-          const uint32_t u = __float_as_uint(v[i] + 0.f);
-          key[i] = max(u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u), 1u);
-          if (cta == 0 && p.logits_out != nullptr)
-            p.logits_out[(size_t)t * p.E + e] = real ? v[i] : 0.f;
-        }
-      }
-      int mine_e = -1;                                  // lane j: the j-th expert and its logit
-      float mine_v = 0.f;
-      if (real) {
-#pragma unroll 1
-        for (int j = 0; j < p.k; ++j) {
-          uint32_t best = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) best = max(best, key[i]);
-          best = __reduce_max_sync(0xffffffffu, best);
-          int e = kMaxExperts;
-#pragma unroll
-          for (int i = 7; i >= 0; --i)
-            if (key[i] == best) e = lane + 32 * i;
-          e = __reduce_min_sync(0xffffffffu, e);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (e == lane + 32 * i) key[i] = 0;
-          if (lane == j) {
-            mine_e = e;
-            mine_v = __uint_as_float(best ^ ((best >> 31) ? 0x80000000u : 0xffffffffu));
-          }
-        }
-      }
-      const float top = __shfl_sync(0xffffffffu, mine_v, 0);
-      const float ex = real && lane < p.k ? expf(mine_v - top) : 0.f;
-      float z = ex;
-      if (!p.renorm) {
-        z = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (lane + 32 * i < p.E) z += expf(v[i] - top);
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-      if (lane < p.k) {
-        const float w = real ? ex / z : 0.f;
-        s.ids[t][lane] = mine_e;
-        s.w[t][lane] = w;
-        if (real) atomicOr(&s.bitmap[mine_e >> 5], 1u << (mine_e & 31));
-        if (cta == 0 && p.ids_out != nullptr) p.ids_out[t * p.k + lane] = mine_e;
-        if (cta == 0 && p.w_out != nullptr) p.w_out[t * p.k + lane] = w;
-      }
+      if (p.E <= 32)
+        select<1>(s, p, logits, t);
+      else if (p.E <= 64)
+        select<2>(s, p, logits, t);
+      else
+        select<8>(s, p, logits, t);
     }
     ws_workers_sync();
     auto rank_of = [&](int e) {
@@ -291,159 +402,94 @@ __device__ __forceinline__ void few_compute(FewSmem<FP8>& s, const FewArgs& p, i
     ws_clear_partial(ws_partial(down_parts, p.T, cta, true), p.T);
   }
 
-  auto on = [&](int slot, int t) { return t < p.T && s.pick[slot][t] >= 0; };
   auto h_row = [&](int slot, int t) {                 // its high part; the low one kTokens below
     return (size_t)((slot == kShared ? 0 : slot + p.S) * kParts * kTokens + t);
   };
-  // a worker's token and its place among the token's sixteen threads
-  const int t_mine = tid >> 4, part_mine = tid & 15;
-  const int t_lane = lane & (kTokens - 1);            // a promoter lane's token
 
-  // ---- 2b. gate/up: columns 0 .. 127 of a tile are gate values, 128 .. 255 up values
-  auto gate_up = [&](bool routed, int I, int experts, float* parts) {
-    const int ft = I / 128;
-    const WsSplit split(experts * ft, ch_h, ctas);
-    const int u1 = split.begin(cta + 1);
-    for (int u = split.begin(cta); u < u1;) {
-      const int tile = u / ch_h, c0 = u - tile * ch_h, c1 = min(ch_h, c0 + (u1 - u)), t0 = u - c0;
-      u += c1 - c0;
-      const int slot = routed ? tile / ft : kShared, f = (routed ? tile - slot * ft : tile) * 128;
-      if (promoter) {
-        sum.clear();
-        if (FP8) {
-          for (int c = c0; c < c1; ++c) sum.template add<true>(1.f, lane < p.T);
-        } else {
-          sum.template add<false>(1.f, lane < p.T);
-        }
-      }
-      ws_tile_free();
-      if (promoter) sum.park(kTokens);
-      ws_tile_ready();
-      if (!worker) continue;
-      // the first of its CTAs finishes a shared tile
-      const WsShare share(split, t0, ch_h);
-      if (cta != share.b0) {
-        ws_store_partial(s.ws.tile, ws_partial(parts, p.T, cta, false), p.T);
-        continue;
-      }
-      const bool mine = on(slot, t_mine);
-      float g[8] = {}, up[8] = {};
-      if (mine) {
-        ws_tile_values(s.ws.tile[t_mine], parts, p.T, share, t_mine, 8 * part_mine, sum.role, g);
-        ws_tile_values(s.ws.tile[t_mine], parts, p.T, share, t_mine, 128 + 8 * part_mine, sum.role,
-                       up);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = g[i] / (1.0f + expf(-g[i])) * up[i];
-      const size_t at = h_row(slot, t_mine) * p.imax + f + 8 * part_mine;
-      if (FP8) {
-        // the tile's 128 features are one group of each token, held by sixteen threads
-        float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(g[i]));
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1)
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-        const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = __fdiv_rn(g[i], sc);
-        if (mine) {
-          *reinterpret_cast<uint2*>(p.h + at) = make_uint2(e4m3_codes4(g[0], g[1], g[2], g[3]),
-                                                           e4m3_codes4(g[4], g[5], g[6], g[7]));
-          if (part_mine == 0) p.sh[h_row(slot, t_mine) * kb_i + f / 128] = sc;
-        }
-      } else if (mine) {
-        // h = high + low, each the nearest bf16 of what is left: 16 bits of fraction
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          hi[i] = two_bf16(g[2 * i], g[2 * i + 1]);
-          lo[i] = two_bf16(g[2 * i] - __uint_as_float(hi[i] << 16),
-                           g[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u));
-        }
-        uint8_t* o = p.h + at * EB;
-        *reinterpret_cast<uint4*>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(o + (size_t)kTokens * p.imax * EB) =
-            make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-    }
-  };
-  // the promoters are at the shared expert while the workers still select the routed ones
+  // Finished tiles: gate/up of the shared expert, of the routed ones, down.
   int A = 0;
 #pragma unroll 1                                      // one copy of the code
-  for (int routed = 0; routed < 2; ++routed) {
+  for (int step = 0; step < 3; ++step) {
+    const bool routed = step == 1, down = step == 2;
     if (routed) {
       ws_tile_free();                                 // now the selection is known to both
-#pragma unroll
-      for (int i = 0; i < kMaxExperts / 32; ++i) A += __popc(s.bitmap[i]);
+      A = few_active(s);
     }
-    gate_up(routed, routed ? p.I : p.Is, routed ? A : p.S,
-            ws_partial(p.part, p.T, 0, routed));
-  }
-  if (worker) {
-    fence_proxy_async();                              // h is read by TMA
-    grid_sync(p.bar + 1);
-    if (tid == 0) mbar_arrive(smem_u32(&s.met));
-  }
-
-  // ---- 3. down and combine
-  if (A == 0) {                                       // every row is padding
-    if (!worker) return;
-    const int n = p.T * p.H / 8;
-    for (int i = cta * kWsThreads + tid; i < n; i += ctas * kWsThreads)
-      reinterpret_cast<uint4*>(p.out)[i] = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const int per = ch_s + A * ch_i;
-  const WsSplit split((p.H + kWsRows - 1) / kWsRows, per, ctas);
-  const int u1 = split.begin(cta + 1);
-  for (int u = split.begin(cta); u < u1;) {
-    const int tile = u / per, c0 = u - tile * per, c1 = min(per, c0 + (u1 - u)), t0 = u - c0;
-    u += c1 - c0;
-    if (promoter) {
-      sum.clear();
-      for (int c = c0; c < c1;) {
-        // the run of stages of one slot
-        const int slot = c < ch_s ? kShared : (c - ch_s) / ch_i;
-        const int first = slot == kShared ? 0 : ch_s + slot * ch_i;
-        const int end = min(c1, first + (slot == kShared ? ch_s : ch_i));
-        // a token that did not select this expert takes nothing from it, not even 0 * inf
-        const bool take = (!FP8 || lane < kTokens) && on(slot, t_lane);
-        const float f = take && slot != kShared ? s.w[t_lane][(int)s.pick[slot][t_lane]] : 1.f;
-        if (FP8) {
-          for (; c < end; ++c) sum.template add<true>(f, take);
+    if (down) {
+      fence_proxy_async();                            // h is read by TMA
+      if (tid == 0) mbar_arrive(smem_u32(&s.drained));
+      arrive(p.bar + 1);
+      meet(p.bar + 1);
+      if (tid == 0) mbar_arrive(smem_u32(&s.met));
+      if (A == 0) {                                   // every row is padding
+        const int n = p.T * p.H / 8;
+        for (int i = cta * kWsThreads + tid; i < n; i += ctas * kWsThreads)
+          reinterpret_cast<uint4*>(p.out)[i] = make_uint4(0, 0, 0, 0);
+        return;
+      }
+    }
+    const int I = routed ? p.I : p.Is, ft = I / 128;
+    const int per = down ? ch_s + A * ch_i : ch_h;
+    const int tiles = down ? (p.H + kWsRows - 1) / kWsRows : routed ? A * ft : p.S * ft;
+    float* const parts = down ? down_parts : ws_partial(p.part, p.T, 0, routed);
+    const WsSplit split(tiles, per, ctas);
+    ws_each_run(split, per, [&](int tile, int, int, int t0) {
+      ws_tile_free();
+      ws_tile_ready();
+      const WsShare share(split, t0, per);
+      // ---- 3. down and combine
+      if (down) {
+        const int n = share.finishers();
+        if (share.b0 != share.b1 && (cta == share.b1 || n > 1))
+          ws_store_partial(s.ws.tile, ws_partial(parts, p.T, cta, cta == share.b0), p.T);
+        if (share.b0 != share.b1 && cta == share.b1) return;
+        // an n-th of the columns, four a thread
+        const int q0 = (kWsRows / 4) * (cta - share.b0) / n, q1 = (kWsRows / 4) * (cta - share.b0 + 1) / n;
+#pragma unroll 1
+        for (int i = tid; i < p.T * (q1 - q0); i += kWsThreads) {
+          const int t = i / (q1 - q0), col = 4 * (q0 + i - t * (q1 - q0));
+          if (tile * kWsRows + col >= p.H) continue;
+          float v[4];
+          ws_tile_values(s.ws.tile[t], parts, p.T, share, t, col, role, v);
+          const bool real = s.ids[t][0] >= 0;
+          *reinterpret_cast<uint2*>(p.out + (size_t)t * p.H + tile * kWsRows + col) =
+              make_uint2(real ? two_bf16(v[0], v[1]) : 0u, real ? two_bf16(v[2], v[3]) : 0u);
+        }
+        return;
+      }
+      // ---- 2b. gate/up: columns 0 .. 127 of a tile are gate values, 128 .. 255 up values; the
+      // first of its CTAs finishes a shared tile
+      const int slot = routed ? tile / ft : kShared, f = (routed ? tile - slot * ft : tile) * 128;
+      if (cta != share.b0) {
+        ws_store_partial(s.ws.tile, ws_partial(parts, p.T, cta, false), p.T);
+        return;
+      }
+      // a warp a token, four features a lane
+#pragma unroll 1
+      for (int t = warp; t < p.T; t += kWsWorkers) {
+        if (!few_on(s, p, slot, t)) continue;
+        float v[8], h[4];
+        ws_tile_values<8, 4, 128>(s.ws.tile[t], parts, p.T, share, t, 4 * lane, role, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = v[i] / (1.0f + expf(-v[i])) * v[4 + i];
+        const size_t row = h_row(slot, t), at = row * p.imax + f + 4 * lane;
+        if (FP8) {                                    // the tile's 128 features are a group
+          float sc;
+          *reinterpret_cast<uint32_t*>(p.h + at) = quantize_group_lane(h, &sc);
+          if (lane == 0) p.sh[row * kb_i + f / 128] = sc;
         } else {
-          sum.template add<false>(f, take);
-          c = end;
+          // h = high + low, each the nearest bf16 of what is left: 16 bits of fraction
+          const uint32_t hi0 = two_bf16(h[0], h[1]), hi1 = two_bf16(h[2], h[3]);
+          const uint32_t lo0 = two_bf16(h[0] - __uint_as_float(hi0 << 16),
+                                        h[1] - __uint_as_float(hi0 & 0xffff0000u));
+          const uint32_t lo1 = two_bf16(h[2] - __uint_as_float(hi1 << 16),
+                                        h[3] - __uint_as_float(hi1 & 0xffff0000u));
+          uint8_t* o = p.h + at * EB;
+          *reinterpret_cast<uint2*>(o) = make_uint2(hi0, hi1);
+          *reinterpret_cast<uint2*>(o + (size_t)kTokens * p.imax * EB) = make_uint2(lo0, lo1);
         }
       }
-      if (!FP8) {                                     // high and low part of h
-#pragma unroll
-        for (int i = 0; i < kWsCols; ++i)
-          sum.acc[i] += __shfl_down_sync(0xffffffffu, sum.acc[i], kTokens);
-      }
-    }
-    ws_tile_free();
-    if (promoter) sum.park(kTokens);
-    ws_tile_ready();
-    if (!worker) continue;
-    const WsShare share(split, t0, per);
-    const int n = share.finishers();
-    if (share.b0 != share.b1 && (cta == share.b1 || n > 1))
-      ws_store_partial(s.ws.tile, ws_partial(down_parts, p.T, cta, cta == share.b0), p.T);
-    if (share.b0 != share.b1 && cta == share.b1) continue;
-    // an n-th of the columns, four a thread
-    const int q0 = (kWsRows / 4) * (cta - share.b0) / n, q1 = (kWsRows / 4) * (cta - share.b0 + 1) / n;
-#pragma unroll 1
-    for (int i = tid; i < p.T * (q1 - q0); i += kWsThreads) {
-      const int t = i / (q1 - q0), col = 4 * (q0 + i - t * (q1 - q0));
-      if (tile * kWsRows + col >= p.H) continue;
-      float v[4];
-      ws_tile_values(s.ws.tile[t], down_parts, p.T, share, t, col, sum.role, v);
-      const bool real = s.ids[t][0] >= 0;
-      *reinterpret_cast<uint2*>(p.out + (size_t)t * p.H + tile * kWsRows + col) =
-          make_uint2(real ? two_bf16(v[0], v[1]) : 0u, real ? two_bf16(v[2], v[3]) : 0u);
-    }
+    });
   }
 }
 
@@ -466,6 +512,7 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
     mbar_init(smem_u32(&s.scored), kWsWorkers);
     mbar_init(smem_u32(&s.ready), 1);
     mbar_init(smem_u32(&s.routed), 1);
+    mbar_init(smem_u32(&s.drained), 1);
     mbar_init(smem_u32(&s.met), 1);
   }
   if (threadIdx.x < kMaxExperts / 32) s.bitmap[threadIdx.x] = 0;
@@ -473,12 +520,6 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
   ws_setup(s.ws);
 
   const WsRole role{p.wait_limit_ns, p.status, p.timeout_bit};
-  auto count_active = [&]() {                         // distinct experts, after the selection
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) n += __popc(s.bitmap[i]);
-    return n;
-  };
   // stage c of a down tile: the slot it reads, and the stage within the slot
   auto down_slot = [&](int c, int* ci) {
     if (c < ch_s) {
@@ -505,9 +546,11 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
     out.role.wait(&s.scored, 0);
     gate_up(&maps.shared_gate_up, p.Is, tiles_s, false);
     if (out.role.wait(&s.routed, 0)) {
-      const int A = count_active();
+      const int A = few_active(s);
       gate_up(&maps.gate_up, p.I, A * (p.I / 128), true);
-      if (A > 0) {
+      // what the last tiles still need from other CTAs would wait behind a ring's worth of
+      // weights
+      if (A > 0 && out.role.wait(&s.drained, 0)) {
         const int per = ch_s + A * ch_i;
         ws_each_unit(down_tiles, per, [&](int tile, int c, bool, bool) {
           int ci;
@@ -521,7 +564,7 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
     out.drain();
   } else if (warp == 2) {
     // ------------------------------------------------------------------ MMA issuer
-    WsMma<FP8, S> mma(s.ws, role);
+    WsMma<S> mma(s.ws, role);
     auto gate_up = [&](int tiles) {
       ws_each_unit(tiles, ch_h, [&](int, int, bool first, bool last) {
         mma.stage(FP8 || first, FP8 || last);
@@ -529,7 +572,7 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
     };
     gate_up(tiles_s);
     if (mma.role.wait(&s.routed, 0)) {
-      const int A = count_active();
+      const int A = few_active(s);
       gate_up(A * (p.I / 128));
       if (A > 0) {
         const int per = ch_s + A * ch_i;
@@ -547,59 +590,48 @@ __global__ void __launch_bounds__(kWsBlock, 1) few_kernel(const __grid_constant_
     const int lane = threadIdx.x & 31, kb_h = p.H / 128;
     auto gate_up = [&](int I, int experts, bool routed) {
       const int ft = I / 128;
-      ws_each_unit_ahead(
-          experts * ft, ch_h,
-          [&](int tile, int c) {
-            WsScale sc;
-            if (FP8) {
-              const int slot = routed ? tile / ft : 0, f = routed ? tile - slot * ft : tile;
-              const float* sw = routed ? p.s_gate_up + (size_t)s.active[slot] * 2 * ft * kb_h
-                                       : p.ss_gate_up;
-              if (lane < p.T) sc.x = __ldcg(p.sx + (size_t)lane * kb_h + c);
-              if (lane < 2) sc.w = __ldg(sw + (size_t)(f + lane * ft) * kb_h + c);
-            }
-            return sc;
-          },
-          [&](int, int c, const WsScale& sc) {
-            out.template load<FP8>(&maps.x, 0, c * kWsBytes, kTokens, sc);
-          });
+      ws_each_unit(experts * ft, ch_h, [&](int tile, int c, bool, bool) {
+        const float *sx = nullptr, *sw = nullptr;
+        if (FP8) {
+          const int slot = routed ? tile / ft : 0, f = routed ? tile - slot * ft : tile;
+          if (lane < p.T) sx = p.sx + (size_t)lane * kb_h + c;
+          if (lane < 2)
+            sw = (routed ? p.s_gate_up + (size_t)s.active[slot] * 2 * ft * kb_h : p.ss_gate_up) +
+                 (size_t)(f + lane * ft) * kb_h + c;
+        }
+        out.load(&maps.x, 0, c * kWsBytes, kTokens, sx, sw);
+      });
     };
     if (FP8 && out.role.wait(&s.ready, 0)) fence_proxy_async();
     gate_up(p.Is, p.S, false);
     if (out.role.wait(&s.routed, 0)) {
-      const int A = count_active();
+      const int A = few_active(s);
       gate_up(p.I, A, true);
       if (A > 0 && out.role.wait(&s.met, 0)) {
         fence_proxy_async();
         const int per = ch_s + A * ch_i, kb_i = p.imax / 128;
-        ws_each_unit_ahead(
-            down_tiles, per,
-            [&](int tile, int c) {
-              WsScale sc;
-              if (FP8) {
-                int ci;
-                const int slot = down_slot(c, &ci), kbs = (slot == kShared ? p.Is : p.I) / 128;
-                const int row = (slot == kShared ? 0 : slot + p.S) * kTokens + lane;
-                const float* sw = slot == kShared
-                                      ? p.ss_down
-                                      : p.s_down + (size_t)s.active[slot] * kb_h * kbs;
-                if (lane < p.T) sc.x = __ldcg(p.sh + (size_t)row * kb_i + ci);
-                // past the end of H the last block, whose sums are not used
-                if (lane < 2) sc.w = __ldg(sw + (size_t)min(2 * tile + lane, kb_h - 1) * kbs + ci);
-              }
-              return sc;
-            },
-            [&](int, int c, const WsScale& sc) {
-              int ci;
-              const int slot = down_slot(c, &ci);
-              out.template load<FP8>(&maps.h, (slot == kShared ? 0 : slot + p.S) * S::ROWS,
-                                     ci * kWsBytes, S::ROWS, sc);
-            });
+        ws_each_unit(down_tiles, per, [&](int tile, int c, bool, bool) {
+          int ci;
+          const int slot = down_slot(c, &ci), place = slot == kShared ? 0 : slot + p.S;
+          const float *sx = nullptr, *sw = nullptr;
+          if (FP8) {
+            const int kbs = (slot == kShared ? p.Is : p.I) / 128;
+            if (lane < p.T) sx = p.sh + (size_t)(place * kTokens + lane) * kb_i + ci;
+            // past the end of H the last block, whose sums are not used
+            if (lane < 2)
+              sw = (slot == kShared ? p.ss_down : p.s_down + (size_t)s.active[slot] * kb_h * kbs) +
+                   (size_t)min(2 * tile + lane, kb_h - 1) * kbs + ci;
+          }
+          out.load(&maps.h, place * S::ROWS, ci * kWsBytes, S::ROWS, sx, sw);
+        });
       }
     }
     out.drain();
   } else {
-    few_compute<FP8>(s, p, ch_h, ch_i, ch_s);
+    if (ws_is_promoter())
+      few_promote<FP8>(s, p, ch_h, ch_i, ch_s);
+    else
+      few_work<FP8>(s, p, ch_h, ch_i, ch_s);
   }
   ws_teardown(s.ws);
 }

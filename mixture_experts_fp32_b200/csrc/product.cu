@@ -50,7 +50,7 @@ __device__ __forceinline__ void store_out4(const ProductArgs& p, int m, int n, c
 
 template <int ROWS>
 struct RowsSmem {
-  WsSmem<ROWS, ROWS, ROWS == 16 ? 6 : 5> ws;          // as many stages as 227 KB hold
+  WsSmem<true, ROWS, ROWS, ROWS == 16 ? 6 : 5> ws;          // as many stages as 227 KB hold
 };
 
 template <int ROWS>
@@ -78,44 +78,40 @@ __global__ void __launch_bounds__(kWsBlock, 1)
     }
     out.drain();
   } else if (warp == 2) {
-    WsMma<true, S> mma(s.ws, role);
+    WsMma<S> mma(s.ws, role);
     for (int u = ub; u < ue; ++u) mma.stage(true, true);
     mma.drain();
   } else if (warp == 3) {
     WsActivations<S> out(s.ws, role);
-    ws_each_unit_ahead(
-        (p.N + kWsRows - 1) / kWsRows, per,
-        [&](int tile, int c) {
-          WsScale sc;
-          if (lane < p.M) sc.x = __ldg(p.sa + (size_t)lane * p.kb + c);
-          // past the end of N the last block, whose sums are not used
-          if (lane < 2) sc.w = __ldg(p.sw + (size_t)min(2 * tile + lane, (p.N - 1) / 128) * p.kb + c);
-          return sc;
-        },
-        [&](int, int c, const WsScale& sc) {
-          out.template load<true>(&amap, 0, c * kWsBytes, ROWS, sc);
-        });
+    // past the end of N the last block of weights, whose sums are not used
+    const float* sx = lane < p.M ? p.sa + (size_t)lane * p.kb : nullptr;
+    for (int u = ub; u < ue; ++u) {
+      const int tile = u / per, c = u - tile * per;
+      const float* sw =
+          lane < 2 ? p.sw + (size_t)min(2 * tile + lane, (p.N - 1) / 128) * p.kb + c : nullptr;
+      out.load(&amap, 0, c * kWsBytes, ROWS, sx ? sx + c : nullptr, sw);
+    }
     out.drain();
+  } else if (ws_is_promoter()) {
+    WsPromoter<S> sum(s.ws, role);
+    ws_each_run(split, per, [&](int, int c0, int c1, int) {
+      sum.clear();
+      for (int c = c0; c < c1; ++c) sum.add(1.f, lane < p.M);
+      ws_tile_free();
+      sum.park(ROWS);
+      ws_tile_ready();
+    });
   } else {
     const int tid = ws_worker_thread();
-    const bool worker = tid >= 0, promoter = !worker;
-    WsPromoter<S> sum(s.ws, role);
-    for (int u = ub; u < ue;) {
-      const int tile = u / per, c0 = u - tile * per, c1 = min(per, c0 + (ue - u)), t0 = u - c0;
-      u += c1 - c0;
-      if (promoter) {
-        sum.clear();
-        for (int c = c0; c < c1; ++c) sum.template add<true>(1.f, lane < p.M);
-      }
+    WsRole wait = role;
+    ws_each_run(split, per, [&](int tile, int, int, int t0) {
       ws_tile_free();
-      if (promoter) sum.park(ROWS);
       ws_tile_ready();
-      if (!worker) continue;
       const WsShare share(split, t0, per);
       const int parts = share.finishers();
       if (share.b0 != share.b1 && (cta == share.b1 || parts > 1))
         ws_store_partial(s.ws.tile, ws_partial(p.part, p.M, cta, cta == share.b0), p.M);
-      if (share.b0 != share.b1 && cta == share.b1) continue;
+      if (share.b0 != share.b1 && cta == share.b1) return;
       // a part of the columns, four of a row a thread at a time
       const int mine = cta - share.b0, q0 = (kWsRows / 4) * mine / parts,
                 q = (kWsRows / 4) * (mine + 1) / parts - q0;
@@ -124,10 +120,10 @@ __global__ void __launch_bounds__(kWsBlock, 1)
         const int m = i / q, col = 4 * (q0 + i - m * q), n = tile * kWsRows + col;
         if (n >= p.N) continue;
         float v[4];
-        ws_tile_values(s.ws.tile[m], p.part, p.M, share, m, col, sum.role, v);
+        ws_tile_values(s.ws.tile[m], p.part, p.M, share, m, col, wait, v);
         store_out4(p, m, n, v);
       }
-    }
+    });
   }
   ws_teardown(s.ws);
 }

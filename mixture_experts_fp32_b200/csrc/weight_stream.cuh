@@ -60,8 +60,9 @@ constexpr int kWsSlots = 16;
 
 // Shared memory of the stream.  ROWS: activation rows brought (16 or 32), TILE: rows of a
 // finished tile.
-template <int ROWS_, int TILE, int STAGES_>
+template <bool FP8_, int ROWS_, int TILE, int STAGES_>
 struct WsSmem {
+  static constexpr bool FP8 = FP8_;
   static constexpr int ROWS = ROWS_, STAGES = STAGES_;
   static_assert(STAGES + 2 < kWsSlots, "slots of scales");
   alignas(1024) uint8_t x[STAGES][ROWS * kWsBytes];   // MMAs read 128 rows from here: into w
@@ -189,7 +190,7 @@ __device__ __forceinline__ void ws_setup(S& s) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::STAGES; ++i) {
       mbar_init(smem_u32(&s.full_w[i]), 1);
-      mbar_init(smem_u32(&s.full_x[i]), 1);
+      mbar_init(smem_u32(&s.full_x[i]), S::FP8 ? 33 : 1);   // and 32 lanes' scales
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -251,10 +252,8 @@ struct WsWeights {
 };
 
 // Activation producer (one warp): the same 128 bytes of K of activation rows row .. + ROWS - 1,
-// FP8 with the stage's scales: x of row `lane`, w of weight block `lane` (0, 1).
-struct WsScale {
-  float x = 0.f, w = 0.f;
-};
+// FP8 with the stage's scales, by asynchronous copies too: lane `i` brings that of row i from
+// sx and, of lanes 0 and 1, that of weight block i from sw (null: none).
 template <class S>
 struct WsActivations {
   S& s;
@@ -264,18 +263,22 @@ struct WsActivations {
   uint64_t policy = policy_evict_last();      // and read again by every CTA
   uint32_t issued = 0, parity = 0;
   __device__ WsActivations(S& s_, const WsRole& r) : s(s_), role(r) {}
-  template <bool FP8>
+  static __device__ __forceinline__ void copy_scale(float* to, const float* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from)
+                 : "memory");
+  }
   __device__ __forceinline__ void load(const CUtensorMap* m, int row, int koff, int box_rows,
-                                       const WsScale& sc) {
+                                       const float* sx, const float* sw) {
     if (!role.wait(&s.empty[pos.i], pos.phase ^ 1u)) return;
-    const int lane = threadIdx.x & 31;
-    if (FP8) {
-      if (lane < S::ROWS) s.scale[slot][lane] = sc.x;
-      if (lane < 2) s.scale[slot][S::ROWS + lane] = sc.w;
+    const uint32_t bar = smem_u32(&s.full_x[pos.i]);
+    if (S::FP8) {
+      const int lane = threadIdx.x & 31;
+      if (sx != nullptr) copy_scale(&s.scale[slot][lane], sx);
+      if (sw != nullptr) copy_scale(&s.scale[slot][S::ROWS + lane], sw);
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
       slot = (slot + 1) % kWsSlots;
       __syncwarp();
     }
-    const uint32_t bar = smem_u32(&s.full_x[pos.i]);
     if (elect_one()) {
       mbar_arrive_expect_tx(bar, box_rows * kWsBytes);
       tma_load_2d(smem_u32(s.x[pos.i]), m, koff, row, bar, policy);
@@ -302,31 +305,21 @@ __device__ __forceinline__ void ws_each_unit(int tiles, int per, F&& f) {
     f(tile, c, u == u0 || c == 0, u + 1 == u1 || c + 1 == per);
   }
 }
-// The same with what `fetch(tile, c)` gives for a unit, asked for four to eight units ahead (a
-// load takes up to two units' time behind a ring's worth of weights).
-template <class G, class F>
-__device__ __forceinline__ void ws_each_unit_ahead(int tiles, int per, G&& fetch, F&& f) {
-  const WsSplit split(tiles, per, gridDim.x);
-  const int u0 = split.begin(blockIdx.x), u1 = split.begin(blockIdx.x + 1);
-  WsScale cur[4], next[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (u0 + j < u1) cur[j] = fetch((u0 + j) / per, (u0 + j) % per);
+// f(tile, c0, c1, t0) for every run of units of one tile: stages c0 .. c1 - 1 of a tile whose
+// first unit is t0.
+template <class F>
+__device__ __forceinline__ void ws_each_run(const WsSplit& split, int per, F&& f) {
+  const int u1 = split.begin(blockIdx.x + 1);
 #pragma unroll 1
-  for (int u = u0; u < u1; u += 4) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (u + 4 + j < u1) next[j] = fetch((u + 4 + j) / per, (u + 4 + j) % per);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (u + j < u1) f((u + j) / per, (u + j) % per, cur[j]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) cur[j] = next[j];
+  for (int u = split.begin(blockIdx.x); u < u1;) {
+    const int tile = u / per, c0 = u - tile * per, c1 = min(per, c0 + (u1 - u));
+    f(tile, c0, c1, u - c0);
+    u += c1 - c0;
   }
 }
 
 // MMA issuer (one warp): stages from `begin` to `end` share a buffer.
-template <bool FP8, class S>
+template <class S>
 struct WsMma {
   S& s;
   WsRole role;
@@ -349,7 +342,7 @@ struct WsMma {
     if (elect_one()) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {           // 32 bytes of K an instruction
-        if (FP8)
+        if (S::FP8)
           umma_e4m3(dst, a + 2 * k, b + 2 * k, idesc_e4m3_m128(kWsRows), k > 0 ? 1u : more);
         else
           umma_bf16(dst, a + 2 * k, b + 2 * k, idesc_bf16_m128(kWsRows), k > 0 ? 1u : more);
@@ -386,12 +379,11 @@ struct WsPromoter {
   }
   // acc += f * the next buffer (FP8: with the stage's scales), in lanes that `take` it; the
   // buffer goes back as soon as it has been read
-  template <bool FP8>
   __device__ __forceinline__ void add(float f, bool take) {
     if (role.wait(&s.dfull[d.i], d.phase)) {
       tc_fence_after();
       const uint32_t at = s.tmem + d.i * kWsRows + (threadIdx.x >> 7) * kWsCols;
-      if (FP8)
+      if (S::FP8)
         f *= s.scale[slot][threadIdx.x & (S::ROWS - 1)] * s.scale[slot][S::ROWS + (threadIdx.x >> 8)];
 #pragma unroll
       for (int c = 0; c < kWsCols; c += 32) {
@@ -409,7 +401,7 @@ struct WsPromoter {
       }
     }
     d.next(2);
-    if (FP8) slot = (slot + 1) % kWsSlots;
+    if (S::FP8) slot = (slot + 1) % kWsSlots;
   }
   // the finished sums into the shared tile, rows 0 .. rows - 1
   __device__ __forceinline__ void park(int rows) {
@@ -461,17 +453,17 @@ __device__ __forceinline__ void ws_store_partial(const float (*tile)[kWsTilePitc
   }
 }
 
-// v = value (row, col) and the V - 1 behind it of a finished tile: this CTA's sums from the
-// shared tile and, where several CTAs share it, the others' partial tiles in CTA order, each
-// awaited.
-template <int V>
+// v = V values of a finished tile's row, RUN from col on and the others GAP columns further:
+// this CTA's sums from the shared tile and, where several CTAs share it, the others' partial
+// tiles in CTA order, each awaited.
+template <int V, int RUN = V, int GAP = 0>
 __device__ __forceinline__ void ws_tile_values(const float* tile_row, float* part, int rows,
                                                const WsShare& sh, int row, int col, WsRole& role,
                                                float (&v)[V]) {
   static_assert(V % 4 == 0, "");
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) {
-    const float4 o = *reinterpret_cast<const float4*>(tile_row + col + 4 * i);
+    const float4 o = *reinterpret_cast<const float4*>(tile_row + col + 4 * i + (4 * i < RUN ? 0 : GAP - RUN));
     v[4 * i] = o.x; v[4 * i + 1] = o.y; v[4 * i + 2] = o.z; v[4 * i + 3] = o.w;
   }
   const int me = blockIdx.x;
@@ -492,7 +484,7 @@ __device__ __forceinline__ void ws_tile_values(const float* tile_row, float* par
           if (other)
             asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
                          : "=f"(o[j][i]), "=f"(o[j][i + 1]), "=f"(o[j][i + 2]), "=f"(o[j][i + 3])
-                         : "l"(at + i)
+                         : "l"(at + i + (i < RUN ? 0 : GAP - RUN))
                          : "memory");
         }
       }
