@@ -21,33 +21,6 @@ struct moe_product_s {
 namespace moe {
 namespace {
 
-// out[m][n .. n + 3], n a multiple of 4, as far as n < N; one store where it is aligned.
-__device__ __forceinline__ void store_out4(const ProductArgs& p, int m, int n, const float (&v)[4]) {
-  const long long at = m * p.ldo + n;
-  if (p.f32) {
-    float* o = static_cast<float*>(p.out) + at;
-    if (n + 3 < p.N && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
-      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < p.N) o[i] = v[i];
-    }
-  } else {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-    if (n + 3 < p.N && (reinterpret_cast<uintptr_t>(o) & 7u) == 0) {
-      *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                                *reinterpret_cast<const uint32_t*>(&b));
-    } else {
-      const __nv_bfloat16 h[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < p.N) o[i] = h[i];
-    }
-  }
-}
-
 template <int ROWS>
 struct RowsSmem {
   WsSmem<true, ROWS, ROWS, ROWS == 16 ? 6 : 5> ws;          // as many stages as 227 KB hold
@@ -121,7 +94,7 @@ __global__ void __launch_bounds__(kWsBlock, 1)
         if (n >= p.N) continue;
         float v[4];
         ws_tile_values(s.ws.tile[m], p.part, p.M, share, m, col, wait, v);
-        store_out4(p, m, n, v);
+        store_out4(p, m, n, make_float4(v[0], v[1], v[2], v[3]));
       }
     });
   }

@@ -28,10 +28,13 @@
 // with the registers warpgroup 0 gives back: a thread has one row (its tensor-memory lane)
 // and 128 columns.
 //
-// Fewer tiles than cluster pairs: K is cut into `splits` parts of a tile; each part stores its
-// sums, and the last of a tile's parts to arrive adds all of them in order, so results do not
-// depend on timing.
+// Fewer tiles than cluster pairs: K is cut into `splits` parts of a tile.  Each stores its sums
+// and, when all have arrived, finishes its part of the columns, adding the parts in order, so
+// results do not depend on timing.  (The last part to arrive finishing all: 256 x 4096 x 7168
+// 31 us.)
 #include <cudaTypedefs.h>
+
+#include <atomic>
 
 #include "product.cuh"
 
@@ -67,7 +70,6 @@ struct TileSmem {
   uint64_t pempty[2][2];                        // even CTA: buffer read by its 8 epilogue warps
   uint64_t teardown;
   uint32_t tmem;
-  int flag;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -261,16 +263,22 @@ __device__ __forceinline__ void store_rows(const ProductArgs& p, uint8_t* stg, i
         }
       } else {
         // rows that begin anywhere: consecutive lanes store consecutive values
-#pragma unroll 1
+        OT v[8][kVals / 32];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < kVals / 32; ++i) {
+            const int e = lane + 32 * i;
+            v[j][i] = *reinterpret_cast<const OT*>(stg + j * 256 + ((e / kChunk ^ j) & 15) * 16 +
+                                                   e % kChunk * sizeof(OT));
+          }
+#pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int m = m0 + rnd * 8 + j;
-          if (m >= p.M) break;
 #pragma unroll
-          for (int e = lane; e < kVals; e += 32) {
-            const int c = e / kChunk, n = n0 + c0 + e;
-            if (n < p.N)
-              out[m * p.ldo + n] = reinterpret_cast<const OT*>(
-                  stg + j * 256 + ((c ^ j) & 15) * 16)[e % kChunk];
+          for (int i = 0; i < kVals / 32; ++i) {
+            const int n = n0 + c0 + lane + 32 * i;
+            if (m < p.M && n < p.N) out[m * p.ldo + n] = v[j][i];
           }
         }
       }
@@ -495,48 +503,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (i + npairs < t.total) first_scales(item_of(i + npairs, t));
-      bool finish = true;
-      const int et = threadIdx.x - 128;               // epilogue thread
-      // this CTA's partial sums of a part of the tile: [column / 4][thread][4]
-      auto part_of = [&](int sp) {
-        return reinterpret_cast<float4*>(p.part) +
-               ((size_t)(it.tile * t.splits + sp) * 2 + rank) * (32 * 256) + et;
-      };
       if (t.splits > 1) {
-        float4* o = part_of(it.split);
+        // this CTA's partial sums of a part of the tile: [column / 4][thread][4]
+        auto part_of = [&](int sp) {
+          return reinterpret_cast<float4*>(p.part) +
+                 ((size_t)(it.tile * t.splits + sp) * 2 + rank) * (32 * 256) + threadIdx.x - 128;
+        };
+        if (warp_live) {
+          float4* o = part_of(it.split);
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          o[c * 256] = make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y);
-        named_bar_sync(1, kEpiWarps * 32);
-        if (et == 0) {
-          unsigned int* counter = p.counters + it.tile * 2 + rank;
-          unsigned int v;
-          asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
-                       : "=r"(v)
-                       : "l"(counter)
-                       : "memory");
-          s.flag = v + 1 == (unsigned int)t.splits;
-          if (s.flag) *counter = 0;
+          for (int c = 0; c < 32; ++c)
+            __stcg(o + c * 256,
+                   make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y));
         }
         named_bar_sync(1, kEpiWarps * 32);
-        finish = s.flag != 0;
-        if (finish) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
-          for (int sp = 0; sp < t.splits; ++sp) {
-            const float4* o2 = part_of(sp);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const float4 v = __ldcg(o2 + c * 256);
-              acc[2 * c].x += v.x;
-              acc[2 * c].y += v.y;
-              acc[2 * c + 1].x += v.z;
-              acc[2 * c + 1].y += v.w;
+        unsigned int* counter = p.counters + it.tile * 2 + rank;
+        if (warp == 4 && elect_one())
+          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
+        if (warp_live && ok) {
+          const uint64_t t0 = global_timer_ns();
+          while (__any_sync(0xffffffffu, ld_acquire_gpu(counter) < (unsigned int)t.splits)) {
+            if (__any_sync(0xffffffffu, global_timer_ns() - t0 >= p.wait_limit_ns)) {
+              if (lane == 0) atomicOr(p.status, kBit);
+              ok = false;
+              break;
             }
           }
+          const int c1 = ok ? 32 * (it.split + 1) / t.splits : 0;
+#pragma unroll 1
+          for (int c0 = 32 * it.split / t.splits; c0 < c1; c0 += 8) {
+            float4 sum[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) sum[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int sp = 0; sp < t.splits; sp += 4) {
+              float4 v[4][8];                         // all on their way at once
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  v[j][c] = sp + j < t.splits && c0 + c < c1
+                                ? __ldcg(part_of(sp + j) + (c0 + c) * 256)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  sum[c].x += v[j][c].x;
+                  sum[c].y += v[j][c].y;
+                  sum[c].z += v[j][c].z;
+                  sum[c].w += v[j][c].w;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              if (m0 + lane < p.M && c0 + c < c1)
+                store_out4(p, m0 + lane, n0 + 4 * (c0 + c), sum[c]);
+          }
         }
-      }
-      if (finish && ok && warp_live) {
+      } else if (ok && warp_live) {
         auto get = [&](int c) { return acc[c]; };
         if (F32)
           store_rows<float>(p, s.stg[warp - 4], m0, n0, get);
@@ -561,6 +586,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // The register shares of the warpgroups only add up if the kernel was built with exactly
 // kLaunchRegs registers a thread; anything else is refused rather than launched (a
 // mismatched split would wait forever).
+std::atomic<int> resident_pairs{kProductPairs};       // clusters a device holds at once, at most
+
 template <bool F32>
 cudaError_t prepare() {
   static_assert(sizeof(TileSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");
@@ -568,9 +595,19 @@ cudaError_t prepare() {
   cudaError_t e = cudaFuncGetAttributes(&attr, product_tiles_kernel<F32>);
   if (e != cudaSuccess) return e;
   if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  return cudaFuncSetAttribute(product_tiles_kernel<F32>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)sizeof(TileSmem) + 1024);
+  e = cudaFuncSetAttribute(product_tiles_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)sizeof(TileSmem) + 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * kProductPairs, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = sizeof(TileSmem) + 1024;
+  int pairs = 0;
+  e = cudaOccupancyMaxActiveClusters(&pairs, product_tiles_kernel<F32>, &cfg);
+  if (e != cudaSuccess) return e;
+  if (pairs < 1) return cudaErrorInvalidConfiguration;
+  if (pairs < resident_pairs.load()) resident_pairs = pairs;
+  return cudaSuccess;
 }
 
 // Row-major bytes [rows, K] as [K / 128][rows][128], in boxes of two columns of `box_rows` rows.
@@ -598,13 +635,14 @@ cudaError_t launch_product_tiles(const ProductArgs& p, int num_sms, cudaStream_t
   t.tiles_m = (p.M + 2 * BM - 1) / (2 * BM);
   const long long tiles = (long long)t.tiles_m * ((p.N + BN - 1) / BN);
   if (tiles > (1 << 29)) return cudaErrorInvalidValue;
-  const int pairs = num_sms / 2 < kProductPairs ? num_sms / 2 : kProductPairs;
-  // Parts of tiles where there are fewer tiles than pairs.  A block of K takes 900 clocks; joining
-  // parts takes 6000 and 1500 a part (28 tiles of 16 blocks: 21 us whole, 24 us in halves).
+  const int most = resident_pairs.load(), pairs = num_sms / 2 < most ? num_sms / 2 : most;
+  // Parts of tiles where there are fewer tiles than pairs.  A block of K takes 800 clocks, joining
+  // n parts 10000 (the partial sums' way) and 20000 / n (the finishing) and 500 n (16 tiles of 56
+  // blocks: 22.6 us in four parts, 33 whole; 37 tiles of 28 blocks: 27 us in halves, 21 whole).
   int splits = 1;
   if (tiles < pairs) {
     const auto cost = [&](int n) {
-      return (p.kb + n - 1) / n * 900 + (n > 1 ? 6000 + 1500 * n : 0);
+      return (p.kb + n - 1) / n * 800 + (n > 1 ? 10000 + 20000 / n + 500 * n : 0);
     };
     for (int n = 2; n * tiles <= pairs && n <= p.kb; ++n)
       if (cost(n) < cost(splits)) splits = n;
@@ -616,11 +654,18 @@ cudaError_t launch_product_tiles(const ProductArgs& p, int num_sms, cudaStream_t
   const int grid = 2 * (t.total < pairs ? t.total : pairs);
   const cudaError_t e = cudaMemsetAsync(p.status, 0, product_head_bytes(p), st);
   if (e != cudaSuccess) return e;
-  if (p.f32)
-    product_tiles_kernel<true><<<grid, kThreads, sizeof(TileSmem) + 1024, st>>>(ma, mw, t);
-  else
-    product_tiles_kernel<false><<<grid, kThreads, sizeof(TileSmem) + 1024, st>>>(ma, mw, t);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = sizeof(TileSmem) + 1024;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];                        // the parts of a tile wait for one another
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = t.splits > 1 ? 1 : 0;
+  return p.f32 ? cudaLaunchKernelEx(&cfg, product_tiles_kernel<true>, ma, mw, t)
+               : cudaLaunchKernelEx(&cfg, product_tiles_kernel<false>, ma, mw, t);
 }
 
 }  // namespace moe
