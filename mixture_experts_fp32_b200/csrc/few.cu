@@ -36,6 +36,7 @@ namespace {
 constexpr int kShared = kFewSlots;                    // slot of the shared expert
 
 constexpr int kTokens = MOE_FEW_TOKENS_MAX;           // rows of every product
+constexpr int kSelected = 4;                          // named barrier: workers arrive, promoters wait
 
 template <bool FP8>
 struct FewSmem {
@@ -193,7 +194,7 @@ __device__ __forceinline__ void few_promote(FewSmem<FP8>& s, const FewArgs& p, i
 #pragma unroll 1                                      // one copy of the code
   for (int routed = 0; routed < 2; ++routed) {
     if (routed) {
-      ws_tile_free();                                 // now the selection is known to both
+      named_bar_sync(kSelected, kWsThreads + 128);
       A = few_active(s);
     }
     const int tiles = routed ? A * (p.I / 128) : p.S * (p.Is / 128);
@@ -398,6 +399,9 @@ __device__ __forceinline__ void few_work(FewSmem<FP8>& s, const FewArgs& p, int 
     if (tid < p.T && s.ids[tid][0] >= 0) s.pick[kShared][tid] = 0;
     ws_workers_sync();
     if (tid == 0) mbar_arrive(smem_u32(&s.routed));
+    // the promoters learn of it without waiting for what the workers do next (a tile of the shared
+    // expert that other CTAs share takes them up to 6 us beside full rings)
+    asm volatile("bar.arrive %0, %1;" ::"n"(kSelected), "n"(kWsThreads + 128) : "memory");
     ws_clear_partial(ws_partial(down_parts, p.T, cta, false), p.T);
     ws_clear_partial(ws_partial(down_parts, p.T, cta, true), p.T);
   }
@@ -411,10 +415,7 @@ __device__ __forceinline__ void few_work(FewSmem<FP8>& s, const FewArgs& p, int 
 #pragma unroll 1                                      // one copy of the code
   for (int step = 0; step < 3; ++step) {
     const bool routed = step == 1, down = step == 2;
-    if (routed) {
-      ws_tile_free();                                 // now the selection is known to both
-      A = few_active(s);
-    }
+    if (routed) A = few_active(s);
     if (down) {
       fence_proxy_async();                            // h is read by TMA
       if (tid == 0) mbar_arrive(smem_u32(&s.drained));
