@@ -8,8 +8,9 @@
 // (launches, ramps and tails of each, the permutation) is what this kernel takes out.
 // One cooperative launch, one CTA per SM, in three phases separated by two grid barriers:
 //
-//   1. router: an (expert, K split) item a CTA, fp32 dot products on the FMA units (7 MB
-//      of weights at most).  FP8: x is quantised per 1x128 group here.
+//   1. router: eight experts and a split of K a CTA, on warp-wide MMAs with the fp32 weights
+//      in three bf16 parts (7 MB of weights at most).  FP8: x is quantised per 1x128 group
+//      here.
 //   2. every CTA selects the experts of all tokens itself (a warp a token; reading T * E
 //      logits from L2 is cheaper than another barrier), then gate/up over the distinct
 //      experts that some token selected: a tile is 128 features, their 128 gate rows and 128
@@ -21,11 +22,18 @@
 //
 // Weights arrive through the ring of weight_stream.cuh, whose producer runs ahead through
 // the barriers: the shared expert's gate/up rows load during the router phase, and the
-// first down rows while the CTAs meet after gate/up.  h lies in rows [expert slot][token], so
-// that the tokens of an expert are one TMA box.  It keeps fp32's precision as two bf16 parts
+// first down rows while the CTAs meet after gate/up, though not before the CTA's own part
+// of h is made.  h lies in rows [expert slot][token], so that the tokens of an expert are
+// one TMA box.  It keeps fp32's precision as two bf16 parts
 // (bf16 weights; the parts are rows of the same product, which costs nothing), or is
 // quantised per 1x128 group, a tile's features (FP8).  Every sum is fp32 and in an order fixed
 // by the shapes and the routing.
+//
+// Measured: one token through 3 of 48 experts and the shared one (882 MB of bf16 weights) in
+// 142 us, 6200 GB/s; through 8 of 256 and the shared one (404 MB of e4m3) in 79 us, 5100 GB/s;
+// 13 tokens through 35 of 40 small experts (119 MB) in 38 us, of which 18 are the weights',
+// 8 the router and selection, and the rest the meetings and the first loads after them.
+// Nothing but those: 16 tokens through 8 experts of 200 KB take 25 us.
 #include <cudaTypedefs.h>
 
 #include "weight_stream.cuh"

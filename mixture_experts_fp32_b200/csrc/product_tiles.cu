@@ -14,9 +14,8 @@
 //
 // A tile is 256 rows x 256 features, by the two CTAs of a cluster with cta_group::2 MMAs: each
 // stages its own 128 rows of A and one half (128 rows) of the weights, 32 KB of shared
-// memory a block, and receives its 128 rows x 256 columns in its own tensor memory.  (A
-// one-CTA 128 x 256 tile stages 48 KB and ran its MMAs at 57 % of the tensor core's rate
-// even without any scales.)  The even CTA issues the MMAs and owns the stage barriers; the
+// memory a block where a one-CTA 128 x 256 tile stages 48, and receives its 128 rows x 256
+// columns in its own tensor memory.  The even CTA issues the MMAs and owns the stage barriers; the
 // odd CTA's loads complete there, and its epilogue warps return buffers by remote arrivals.
 // No load is multicast.
 //

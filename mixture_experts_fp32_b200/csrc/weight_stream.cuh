@@ -11,11 +11,16 @@
 //  - tcgen05 multiplies straight from shared memory, so that no instruction handles a
 //    single weight, with the weights on the N side (256) and the few activation rows on the
 //    M side (128, of which the rest is whatever lies behind them in shared memory: rows of
-//    a product do not meet).  An MMA of 128 rows took 130 (bf16) to 220 (e4m3) clocks
-//    whatever its N, so weights on the M side would pass at 31 or 19 bytes a clock; the
-//    same product with warp-wide mma.sync took 330 instructions a warp and stage;
+//    a product do not meet).  Four MMAs of 128 x 256 take 512 clocks, so a stage's weights
+//    pass at 64 bytes a clock, and a finished row lies in one tensor-memory lane, its columns
+//    at a promoter's hand.  With weights on the M side the few columns would make the
+//    MMAs' least time, 45 clocks each whatever N, count twice, and spread a row over lanes.
+//    The same product with warp-wide mma.sync took 330 instructions a warp and stage;
 //  - a second producer brings the activation rows, so that weights can be under way before
 //    the activations they will meet have been computed;
+//  - what a launch runs once waits for its instructions longer than it runs, and beside full
+//    rings every trip to L2 takes up to 4 us: the code between the phases is short loops and
+//    its loads go out together;
 //  - block scales change every 128 bytes of K (FP8): each stage is multiplied into one of
 //    two tensor-memory buffers, and four promoter warps (the ones that can read the first
 //    32 lanes, 64 columns each) add it to their fp32 sums with its scale.  Otherwise a
@@ -84,8 +89,9 @@ bool ws_map_nd(CUtensorMap* m, const void* w, int rank, const uint64_t* dims,
 
 // The split of `tiles` tiles of `per` units over the CTAs: contiguous ranges, the first `more`
 // CTAs one unit more than `each`, the CTAs behind the last unit none.  Even over all CTAs,
-// unless that leaves one fewer than kWsLeast units: a shared tile costs its CTAs about what
-// four units take, so small work goes to fewer CTAs, whole tiles where these are short.
+// unless that leaves one fewer than kWsLeast units: sharing a tile costs its CTAs a trip
+// through L2, 2000 clocks or more where a unit takes 800 to 1400, so small work goes to fewer
+// CTAs, whole tiles where these are short.
 constexpr int kWsLeast = 3;
 struct WsSplit {
   int each, more;
