@@ -216,8 +216,9 @@ typedef enum {
  * elements and holds cols values v, or with gated = 1 cols values g and then cols values u,
  * and v = silu(g) * u in fp32.  For every group of 128 consecutive columns (the last one
  * may be shorter):
- *   scales[r, group] = amax / 448 over the group's |v| (fp32; 1 where amax = 0)
- *   codes[r, c]      = the e4m3 value nearest v / scale (fp32 division, ties to even)
+ *   scales[r, group] = amax / 448 over the group's |v| (fp32; 1 where that is 0)
+ *   codes[r, c]      = the e4m3 value nearest v / scale (fp32 division, ties to even, at most
+ *                      448: a subnormal scale is coarse)
  * codes: e4m3 bytes [rows, cols], scales: fp32 [rows, ceil(cols / 128)], both dense.  Rows
  * with valid[r] = 0 (valid: uint8 [rows] or NULL) are padding: their contents are not read,
  * their codes are 0 and their scales 1, so a product with them gives zero rows.  A NaN

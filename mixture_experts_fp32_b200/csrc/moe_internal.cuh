@@ -217,12 +217,13 @@ __device__ __forceinline__ uint32_t e4m3_codes4(float a, float b, float c, float
 }
 
 // One 1x128 group by one warp, four values a lane: returns the lane's codes, sets the
-// group's scale (amax / 448; 1 if every value is zero).
+// group's scale (amax / 448; 1 where that is zero).
 __device__ __forceinline__ uint32_t quantize_group_lane(const float (&v)[4], float* scale) {
   float a = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-  const float s = a > 0.f ? __fdiv_rn(a, 448.f) : 1.f;
+  float s = __fdiv_rn(a, 448.f);
+  if (s == 0.f) s = 1.f;
   *scale = s;
   return e4m3_codes4(__fdiv_rn(v[0], s), __fdiv_rn(v[1], s), __fdiv_rn(v[2], s),
                      __fdiv_rn(v[3], s));

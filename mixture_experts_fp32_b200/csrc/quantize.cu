@@ -1,6 +1,6 @@
 // e4m3 quantisation per 1x128 group, of x or of silu(g) * u (moe_quantize_groups).
 //
-// s = amax / 448 over the group's values (1 if they are all zero), codes the e4m3 values
+// s = amax / 448 over the group's values (1 where that is zero in fp32), codes the e4m3 values
 // nearest v / s; the sums of products they enter are bound by the codes' 3 bits of
 // fraction, so everything before the code is fp32.  Bound by HBM: one read of the values,
 // one write of the codes.  Eight lanes take a group, 16 consecutive values a lane: 16-byte
@@ -10,10 +10,10 @@
 // two codes), but sixteen divisions a lane cost more than the bytes.  They take one
 // reciprocal a lane and four fused multiply-adds a value instead (quotient below), two values
 // an instruction; the next group's loads are on their way meanwhile.  Instructions still bound
-// it more than bytes (7168 columns of 8192 rows of bf16: 40 us, 4400 GB/s; one group at a time
-// with divisions 51 us).  Gated values take more registers than let four blocks share an SM:
-// held to 64 they spill a little and are faster for it (fp32, 4099 rows of 2 x 2064, 900 of them
-// padding: 19 against 21 us).
+// it more than bytes (7168 columns of 8192 rows of bf16: 42 us, 4200 GB/s; one group at a time
+// with divisions 51 us).  Registers are held to 64, so that four blocks share an SM: gated
+// values spill a little and are faster for it (fp32, 4099 rows of 2 x 2064, 900 of them
+// padding: 19 against 21 us), the others 42 against 46.
 #include "moe_internal.cuh"
 
 #define MOE_EXPORT extern "C" __attribute__((visibility("default")))
@@ -36,18 +36,21 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < N; ++i) w[i] = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void values(float2 (&v)[kVals / 2]) const {
+  // -v: what the quotients start from
+  __device__ __forceinline__ void negated(float2 (&v)[kVals / 2]) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const uint32_t r[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
       if (sizeof(XT) == 2) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          v[4 * i + j] =
-              make_float2(__uint_as_float(r[j] << 16), __uint_as_float(r[j] & 0xffff0000u));
+          {
+            const uint32_t n = r[j] ^ 0x80008000u;
+            v[4 * i + j] = make_float2(__uint_as_float(n << 16), __uint_as_float(n & 0xffff0000u));
+          }
       } else {
-        v[2 * i] = make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
-        v[2 * i + 1] = make_float2(__uint_as_float(r[2]), __uint_as_float(r[3]));
+        v[2 * i] = make_float2(-__uint_as_float(r[0]), -__uint_as_float(r[1]));
+        v[2 * i + 1] = make_float2(-__uint_as_float(r[2]), -__uint_as_float(r[3]));
       }
     }
   }
@@ -67,7 +70,7 @@ struct Raw {
       return fmaxf(__low2float(m), __high2float(m));
     }
     float2 v[kVals / 2];
-    values(v);
+    negated(v);
     return largest(v);
   }
   static __device__ __forceinline__ float largest(const float2 (&v)[kVals / 2]) {
@@ -81,13 +84,13 @@ struct Raw {
 // RN(v / s) from r = RN(1 / s) by Markstein's method: a quotient within an ulp (the first
 // correction makes it so) plus r times its exact remainder rounds to the correctly rounded
 // quotient.  For s in [2^-70, 2^100] and |v| <= 448 s: no step then overflows, and none
-// underflows for a quotient that has a code other than 0.
-// (Two values an instruction.)
-__device__ __forceinline__ float2 quotient(float2 v, float s, float r) {
-  const float2 r2 = make_float2(r, r), n2 = make_float2(-s, -s);
-  const float2 q0 = __fmul2_rn(v, r2);
-  const float2 q1 = __ffma2_rn(__ffma2_rn(q0, n2, v), r2, q0);
-  return __ffma2_rn(__ffma2_rn(q1, n2, v), r2, q1);
+// underflows for a quotient that has a code other than 0.  Two values an instruction; they start
+// from n = -v and correct by n + q s, so that a quotient of -0 stays one.
+__device__ __forceinline__ float2 quotient(float2 n, float s, float r) {
+  const float2 s2 = make_float2(s, s), nr2 = make_float2(-r, -r);
+  const float2 q0 = __fmul2_rn(n, nr2);
+  const float2 q1 = __ffma2_rn(__ffma2_rn(q0, s2, n), nr2, q0);
+  return __ffma2_rn(__ffma2_rn(q1, s2, n), nr2, q1);
 }
 
 // silu(g) * u; the quotient of silu by the same method (d = 1 + e^-g >= 1; above 2^100 the
@@ -102,7 +105,7 @@ __device__ __forceinline__ float gated_value(float g, float u) {
 
 // IT: type of the group index (int where rows * groups allows it)
 template <typename XT, bool GATED, typename IT>
-__global__ void __launch_bounds__(256, GATED ? 4 : 3) quantize_groups_kernel(
+__global__ void __launch_bounds__(256, 4) quantize_groups_kernel(
     const XT* __restrict__ x, const uint8_t* __restrict__ valid, int rows, int cols, long long ldx,
     uint8_t* __restrict__ codes, float* __restrict__ scales) {
   const int groups = (cols + 127) / 128;
@@ -133,14 +136,14 @@ __global__ void __launch_bounds__(256, GATED ? 4 : 3) quantize_groups_kernel(
   fetch(u);
   for (IT it = 0; it < rounds; ++it, u += step) {
     float2 v[kVals / 2];
-    raw.values(v);
+    raw.negated(v);
     float amax;
     if (GATED) {
       float2 up[kVals / 2];
-      raw_up.values(up);
+      raw_up.negated(up);
 #pragma unroll
       for (int i = 0; i < kVals / 2; ++i)
-        v[i] = make_float2(gated_value(v[i].x, up[i].x), gated_value(v[i].y, up[i].y));
+        v[i] = make_float2(gated_value(-v[i].x, up[i].x), gated_value(-v[i].y, up[i].y));
       amax = Raw<XT>::largest(v);
     } else {
       amax = raw.amax();
@@ -152,7 +155,8 @@ __global__ void __launch_bounds__(256, GATED ? 4 : 3) quantize_groups_kernel(
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1)
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    float sc = __fdiv_rn(amax, 448.f);
+    if (sc == 0.f) sc = 1.f;                          // of values all zero, or next to it
     if (sc >= 0x1p-70f && sc <= 0x1p100f) {
       const float r = __frcp_rn(sc);
 #pragma unroll
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(256, GATED ? 4 : 3) quantize_groups_kernel(
     } else {
 #pragma unroll
       for (int i = 0; i < kVals / 2; ++i)
-        v[i] = make_float2(__fdiv_rn(v[i].x, sc), __fdiv_rn(v[i].y, sc));
+        v[i] = make_float2(__fdiv_rn(v[i].x, -sc), __fdiv_rn(v[i].y, -sc));
     }
     uint32_t o[4];
 #pragma unroll
