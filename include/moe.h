@@ -246,7 +246,7 @@ moe_status moe_quantize_groups(const void *x, moe_dtype x_type, int rows, int co
  * bounded (moe_product_set_wait_limit, nanoseconds, default 2e9) and report
  * MOE_DEV_WAIT_TIMEOUT_PRODUCT through moe_product_device_status, which synchronises the
  * stream and reads and clears the status word of this workspace, like
- * moe_check_device_status.  Calls whose CTAs wait for one another (at most 32 rows, or so few
+ * moe_check_device_status.  Calls whose CTAs wait for one another (few rows, or so few
  * tiles that K is divided) are cooperative launches, which start when long-running kernels
  * of other streams have left the SMs.  Make the first product on a device outside graph
  * capture. */

@@ -2,8 +2,10 @@
 //
 //   out[m, n] = sum_kb sa[m, kb] * sw[n / 128, kb] * sum_{k in kb} a[m, k] * w[n, k]
 //
-// Here the entry points and the kernel of up to 32 rows: the weights stream once past all of them
-// (weight_stream.cuh); HBM is the bound.  More rows: product_tiles.cu.
+// Here the entry points and the kernel of few rows: the weights stream past blocks of 16 or 32 of
+// them (weight_stream.cuh); HBM is the bound.  A tile is a row block of 256 features, the row
+// blocks of the same features next to one another, so that the weights come from HBM once.
+// More rows: product_tiles.cu.
 #include <string.h>
 
 #include <new>
@@ -37,15 +39,16 @@ __global__ void __launch_bounds__(kWsBlock, 1)
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
   const int per = p.kb;                               // stages of a tile
-  const WsSplit split((p.N + kWsRows - 1) / kWsRows, per, ctas);
+  const int blocks = (p.M + ROWS - 1) / ROWS, part_rows = min(p.M, ROWS);
+  const WsSplit split((p.N + kWsRows - 1) / kWsRows * blocks, per, ctas);
   const int ub = split.begin(cta), ue = split.begin(cta + 1);
   const WsRole role{p.wait_limit_ns, p.status, MOE_DEV_WAIT_TIMEOUT_PRODUCT};
   ws_setup(s.ws);
 
   if (warp == 1) {
-    WsWeights<S> out(s.ws, role);
+    WsWeights<S> out(s.ws, role, blocks > 1);
     for (int u = ub; u < ue; ++u) {
-      const int tile = u / per, row = tile * kWsRows;
+      const int tile = u / per, row = tile / blocks * kWsRows;
       out.load(&wmap, row, row + kWsBoxRows < p.N ? row + kWsBoxRows : -1,
                (u - tile * per) * kWsBytes);
     }
@@ -57,19 +60,20 @@ __global__ void __launch_bounds__(kWsBlock, 1)
   } else if (warp == 3) {
     WsActivations<S> out(s.ws, role);
     // past the end of N the last block of weights, whose sums are not used
-    const float* sx = lane < p.M ? p.sa + (size_t)lane * p.kb : nullptr;
     for (int u = ub; u < ue; ++u) {
-      const int tile = u / per, c = u - tile * per;
-      const float* sw =
-          lane < 2 ? p.sw + (size_t)min(2 * tile + lane, (p.N - 1) / 128) * p.kb + c : nullptr;
-      out.load(&amap, 0, c * kWsBytes, ROWS, sx ? sx + c : nullptr, sw);
+      const int tile = u / per, c = u - tile * per, f = tile / blocks, m0 = (tile - f * blocks) * ROWS;
+      const float *sx = nullptr, *sw = nullptr;
+      if (lane < ROWS && m0 + lane < p.M) sx = p.sa + (size_t)(m0 + lane) * p.kb + c;
+      if (lane < 2) sw = p.sw + (size_t)min(2 * f + lane, (p.N - 1) / 128) * p.kb + c;
+      out.load(&amap, m0, c * kWsBytes, ROWS, sx, sw);
     }
     out.drain();
   } else if (ws_is_promoter()) {
     WsPromoter<S> sum(s.ws, role);
-    ws_each_run(split, per, [&](int, int c0, int c1, int) {
+    ws_each_run(split, per, [&](int tile, int c0, int c1, int) {
+      const bool take = lane < ROWS && tile % blocks * ROWS + lane < p.M;
       sum.clear();
-      for (int c = c0; c < c1; ++c) sum.add(1.f, lane < p.M);
+      for (int c = c0; c < c1; ++c) sum.add(1.f, take);
       ws_tile_free();
       sum.park(ROWS);
       ws_tile_ready();
@@ -83,18 +87,19 @@ __global__ void __launch_bounds__(kWsBlock, 1)
       const WsShare share(split, t0, per);
       const int parts = share.finishers();
       if (share.b0 != share.b1 && (cta == share.b1 || parts > 1))
-        ws_store_partial(s.ws.tile, ws_partial(p.part, p.M, cta, cta == share.b0), p.M);
+        ws_store_partial(s.ws.tile, ws_partial(p.part, part_rows, cta, cta == share.b0), part_rows);
       if (share.b0 != share.b1 && cta == share.b1) return;
       // a part of the columns, four of a row a thread at a time
+      const int f = tile / blocks, m0 = (tile - f * blocks) * ROWS, rows = min(ROWS, p.M - m0);
       const int mine = cta - share.b0, q0 = (kWsRows / 4) * mine / parts,
                 q = (kWsRows / 4) * (mine + 1) / parts - q0;
 #pragma unroll 1
-      for (int i = tid; i < p.M * q; i += kWsThreads) {
-        const int m = i / q, col = 4 * (q0 + i - m * q), n = tile * kWsRows + col;
+      for (int i = tid; i < rows * q; i += kWsThreads) {
+        const int m = i / q, col = 4 * (q0 + i - m * q), n = f * kWsRows + col;
         if (n >= p.N) continue;
         float v[4];
-        ws_tile_values(s.ws.tile[m], p.part, p.M, share, m, col, wait, v);
-        store_out4(p, m, n, make_float4(v[0], v[1], v[2], v[3]));
+        ws_tile_values(s.ws.tile[m], p.part, part_rows, share, m, col, wait, v);
+        store_out4(p, m0 + m, n, make_float4(v[0], v[1], v[2], v[3]));
       }
     });
   }
@@ -108,10 +113,11 @@ cudaError_t launch_rows(const ProductArgs& a, int ctas, cudaStream_t st) {
     return cudaErrorInvalidValue;
   // the status word and, where tiles are shared, the partial tiles: heads, and tails if a tile
   // has more than two CTAs
-  const WsSplit split((a.N + kWsRows - 1) / kWsRows, a.kb, ctas);
+  const int blocks = (a.M + ROWS - 1) / ROWS, part_rows = a.M < ROWS ? a.M : ROWS;
+  const WsSplit split((a.N + kWsRows - 1) / kWsRows * blocks, a.kb, ctas);
   const int slots = split.whole(a.kb) ? 0 : split.each >= a.kb ? kWsCtas : 2 * kWsCtas;
   const cudaError_t e = cudaMemsetAsync(
-      a.status, 0, product_head_bytes(a) + sizeof(float) * slots * a.M * kWsRows, st);
+      a.status, 0, product_head_bytes(a) + sizeof(float) * slots * part_rows * kWsRows, st);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, 1, 1);
@@ -124,6 +130,18 @@ cudaError_t launch_rows(const ProductArgs& a, int ctas, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, product_rows_kernel<ROWS>, wm, am, a);
+}
+
+// Whether row blocks of 32 are quicker than 256-row tiles: a stage of the stream (256 features of a
+// block against 128 K) takes a CTA 900 clocks, the meeting of the CTAs 5000 more than the end
+// of a tile, and the tiles what product_tiles.cu reckons (64 rows of 4096 x 7168: 16.3 us as
+// blocks, 20.1 as tiles; 77 of 1111 x 1200: 12.5 and 20.5; 128 of 7168 x 2048: 18.6 and 16.5).
+bool rows_are_few(const ProductArgs& p, int ctas, int num_sms) {
+  if (p.M <= kProductRows) return true;
+  if (p.M > kProductBlocks * kProductRows) return false;
+  const long long blocks = (p.M + kProductRows - 1) / kProductRows;
+  const long long units = (p.N + kWsRows - 1) / kWsRows * blocks * p.kb;
+  return units < (1 << 30) && (units + ctas - 1) / ctas * 900 + 5000 < product_tiles_clocks(p, num_sms);
 }
 
 template <int ROWS>
@@ -216,9 +234,9 @@ MOE_EXPORT moe_status moe_block_scaled_product(moe_product_t p, const void* a,
   g.out = out;
   g.M = rows;
   const int ctas = sms < moe::kWsCtas ? sms : moe::kWsCtas;
-  return moe::cuda_status(rows > moe::kProductRows ? moe::launch_product_tiles(g, sms, st)
-                          : rows > 16             ? moe::launch_rows<32>(g, ctas, st)
-                                                  : moe::launch_rows<16>(g, ctas, st));
+  return moe::cuda_status(rows <= 16                      ? moe::launch_rows<16>(g, ctas, st)
+                          : moe::rows_are_few(g, ctas, sms) ? moe::launch_rows<32>(g, ctas, st)
+                                                          : moe::launch_product_tiles(g, sms, st));
 }
 
 MOE_EXPORT moe_status moe_product_device_status(moe_product_t product, void* workspace,

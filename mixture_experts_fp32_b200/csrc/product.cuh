@@ -6,7 +6,8 @@
 
 namespace moe {
 
-constexpr int kProductRows = 32;               // rows the weight stream takes
+constexpr int kProductRows = 32;               // rows of a block of the weight stream
+constexpr int kProductBlocks = 4;              // and as many of them at most
 constexpr int kProductPairs = 80;
 constexpr int kProductCounters = 2 * kProductPairs;   // of the tiles' two halves
 
@@ -64,5 +65,7 @@ __device__ __forceinline__ void store_out4(const ProductArgs& p, int m, int n, f
 
 cudaError_t launch_product_tiles(const ProductArgs& p, int num_sms, cudaStream_t st);
 cudaError_t prepare_product_tiles();
+// The clocks that the tiles' work would take, without what every launch takes.
+long long product_tiles_clocks(const ProductArgs& p, int num_sms);
 
 }  // namespace moe

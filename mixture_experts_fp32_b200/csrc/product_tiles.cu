@@ -101,12 +101,22 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar_cluster), "l"(policy)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_pair_3d(uint32_t dst, const CUtensorMap* m, int y, int z,
-                                                 uint32_t bar_cluster, uint64_t policy) {
+__device__ __forceinline__ void tma_load_pair_3d(uint32_t dst, const CUtensorMap* m, int x, int y,
+                                                 int z, uint32_t bar_cluster, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(y), "r"(z), "r"(bar_cluster), "l"(policy)
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar_cluster), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_pair_4d(uint32_t dst, const CUtensorMap* m, int x, int y,
+                                                 int z, int w, uint32_t bar_cluster,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar_cluster),
+      "l"(policy)
       : "memory");
 }
 // D[tmem of both CTAs] (+)= A[smem of both] * B[smem of both]^T, M = 256, N = 128.
@@ -348,13 +358,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(own, 4 * (A_BYTES + B_BYTES));
             if (t.columns) {
-              tma_load_pair_3d(a, &tmA, arow, kb, fb, pol);
-              tma_load_pair_3d(b, &tmW, wrow, kb, fb, pol);
-              tma_load_pair_3d(b + B_BYTES, &tmW, wrow + BH, kb, fb, pol);
+              tma_load_pair_4d(a, &tmA, 0, arow, kb, 0, fb, pol);
+              tma_load_pair_3d(b, &tmW, 0, wrow, kb, fb, pol);
+              tma_load_pair_3d(b + B_BYTES, &tmW, 0, wrow + BH, kb, fb, pol);
             } else {
 #pragma unroll
               for (int j = 0; j < 2; ++j) {           // past the end of K: zeros
-                tma_load_pair(a + j * A_BYTES, &tmA, (kb + j) * BK, arow, fb, pol);
+                tma_load_pair_3d(a + j * A_BYTES, &tmA, (kb + j) * BK, arow, 0, fb, pol);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                   tma_load_pair(b + h * B_BYTES + j * (B_BYTES / 2), &tmW, (kb + j) * BK,
@@ -609,12 +619,46 @@ cudaError_t prepare() {
   return cudaSuccess;
 }
 
-// Row-major bytes [rows, K] as [K / 128][rows][128], in boxes of two columns of `box_rows` rows.
-bool column_map(CUtensorMap* m, const void* w, uint64_t K, uint64_t rows, int box_rows) {
-  const uint64_t dims[3] = {BK, rows, K / BK}, strides[2] = {K, BK};
-  const uint32_t box[3] = {BK, (uint32_t)box_rows, 2};
-  return ws_map_nd(m, w, 3, dims, strides, box);
+// Maps of a tensor of less than 128 KB load these boxes at a fraction of the rate: 40 x 18944 x 2048
+// took 39 us with A's 80 KB mapped as they are, 64 rows (128 KB) 18.5.  So A's maps get one more
+// dimension, of as many copies as 128 KB take, of which only the first is ever addressed (now
+// 18.5 us).  The weight stream's smaller boxes load as well either way.
+uint64_t copies(uint64_t bytes) { return ((1 << 17) + bytes - 1) / bytes; }
+// Row-major bytes [rows, K], in boxes of 128 columns of `box_rows` rows.
+bool row_map(CUtensorMap* m, const void* a, uint64_t K, uint64_t rows, int box_rows) {
+  const uint64_t dims[3] = {K, rows, copies(K * rows)}, strides[2] = {K, K * rows};
+  const uint32_t box[3] = {BK, (uint32_t)box_rows, 1};
+  return ws_map_nd(m, a, 3, dims, strides, box);
 }
+// The same as [K / 128][rows][128], in boxes of two columns; rank 4: with copies.
+bool column_map(CUtensorMap* m, const void* w, uint64_t K, uint64_t rows, int box_rows, int rank) {
+  const uint64_t dims[4] = {BK, rows, K / BK, copies(K * rows)}, strides[3] = {K, BK, K * rows};
+  const uint32_t box[4] = {BK, (uint32_t)box_rows, 2, 1};
+  return ws_map_nd(m, w, rank, dims, strides, box);
+}
+
+// How the tiles are cut: K of each in `splits` parts where there are fewer tiles than pairs.  A block
+// of K takes 800 clocks, joining n parts 10000 (the partial sums' way) and 20000 / n (the
+// finishing) and 500 n (16 tiles of 56 blocks: 22.6 us in four parts, 33 whole; 37 tiles of 28
+// blocks: 27 us in halves, 21 whole).
+struct TilePlan {
+  long long tiles, clocks;
+  int tiles_m, pairs, splits;
+  TilePlan(const ProductArgs& p, int num_sms) {
+    tiles_m = (p.M + 2 * BM - 1) / (2 * BM);
+    tiles = (long long)tiles_m * ((p.N + BN - 1) / BN);
+    const int most = resident_pairs.load();
+    pairs = num_sms / 2 < most ? num_sms / 2 : most;
+    const auto cost = [&](int n) {
+      return (p.kb + n - 1) / n * 800ll + (n > 1 ? 10000 + 20000 / n + 500 * n : 0);
+    };
+    splits = 1;
+    if (tiles < pairs)
+      for (int n = 2; n * tiles <= pairs && n <= p.kb; ++n)
+        if (cost(n) < cost(splits)) splits = n;
+    clocks = (tiles + pairs - 1) / pairs * cost(splits);
+  }
+};
 
 }  // namespace
 
@@ -623,33 +667,27 @@ cudaError_t prepare_product_tiles() {
   return e == cudaSuccess ? prepare<true>() : e;
 }
 
+long long product_tiles_clocks(const ProductArgs& p, int num_sms) {
+  return TilePlan(p, num_sms).clocks;
+}
+
 cudaError_t launch_product_tiles(const ProductArgs& p, int num_sms, cudaStream_t st) {
   TileArgs t;
   t.columns = p.K % BK == 0;
   CUtensorMap ma, mw;
-  if (t.columns ? !column_map(&ma, p.a, p.K, p.M, BM) || !column_map(&mw, p.w, p.K, p.N, BH / 2)
-                : !ws_map(&ma, p.a, p.K, p.M, BM) || !ws_map(&mw, p.w, p.K, p.N, BH / 2))
+  if (t.columns
+          ? !column_map(&ma, p.a, p.K, p.M, BM, 4) || !column_map(&mw, p.w, p.K, p.N, BH / 2, 3)
+          : !row_map(&ma, p.a, p.K, p.M, BM) || !ws_map(&mw, p.w, p.K, p.N, BH / 2))
     return cudaErrorInvalidValue;
+  const TilePlan plan(p, num_sms);
+  if (plan.tiles > (1 << 29)) return cudaErrorInvalidValue;
+  const int pairs = plan.pairs, splits = plan.splits;
   t.p = p;
-  t.tiles_m = (p.M + 2 * BM - 1) / (2 * BM);
-  const long long tiles = (long long)t.tiles_m * ((p.N + BN - 1) / BN);
-  if (tiles > (1 << 29)) return cudaErrorInvalidValue;
-  const int most = resident_pairs.load(), pairs = num_sms / 2 < most ? num_sms / 2 : most;
-  // Parts of tiles where there are fewer tiles than pairs.  A block of K takes 800 clocks, joining
-  // n parts 10000 (the partial sums' way) and 20000 / n (the finishing) and 500 n (16 tiles of 56
-  // blocks: 22.6 us in four parts, 33 whole; 37 tiles of 28 blocks: 27 us in halves, 21 whole).
-  int splits = 1;
-  if (tiles < pairs) {
-    const auto cost = [&](int n) {
-      return (p.kb + n - 1) / n * 800 + (n > 1 ? 10000 + 20000 / n + 500 * n : 0);
-    };
-    for (int n = 2; n * tiles <= pairs && n <= p.kb; ++n)
-      if (cost(n) < cost(splits)) splits = n;
-  }
+  t.tiles_m = plan.tiles_m;
   t.kb_per_split = (p.kb + splits - 1) / splits;
   t.kb_per_split += t.kb_per_split & 1;
   t.splits = (p.kb + t.kb_per_split - 1) / t.kb_per_split;
-  t.total = (int)tiles * t.splits;
+  t.total = (int)plan.tiles * t.splits;
   const int grid = 2 * (t.total < pairs ? t.total : pairs);
   const cudaError_t e = cudaMemsetAsync(p.status, 0, product_head_bytes(p), st);
   if (e != cudaSuccess) return e;

@@ -234,9 +234,11 @@ struct WsWeights {
   S& s;
   WsRole role;
   WsPos pos;
-  uint64_t policy = policy_evict_first();     // weights are read once
+  uint64_t policy;
   uint32_t issued = 0, parity = 0;
-  __device__ WsWeights(S& s_, const WsRole& r) : s(s_), role(r) {}
+  // `again`: other row blocks read the same weights
+  __device__ WsWeights(S& s_, const WsRole& r, bool again = false)
+      : s(s_), role(r), policy(again ? policy_evict_normal() : policy_evict_first()) {}
   __device__ __forceinline__ void load(const CUtensorMap* m, int row0, int row1, int koff) {
     if (!role.wait(&s.empty[pos.i], pos.phase ^ 1u)) return;
     const uint32_t bar = smem_u32(&s.full_w[pos.i]), dst = smem_u32(s.w[pos.i]);
