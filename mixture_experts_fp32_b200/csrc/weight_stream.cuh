@@ -12,9 +12,9 @@
 //    single weight, with the weights on the N side (256) and the few activation rows on the
 //    M side (128, of which the rest is whatever lies behind them in shared memory: rows of
 //    a product do not meet).  Four MMAs of 128 x 256 take 512 clocks, so a stage's weights
-//    pass at 64 bytes a clock, and a finished row lies in one tensor-memory lane, its columns
-//    at a promoter's hand.  With weights on the M side the few columns would make the
-//    MMAs' least time, 45 clocks each whatever N, count twice, and spread a row over lanes.
+//    pass at 64 bytes a clock, and a finished row lies in one tensor-memory lane, which
+//    few promoters reach; weights on the M side would need 360 clocks and four times the
+//    promoters' loads, and neither is what bounds it.
 //    The same product with warp-wide mma.sync took 330 instructions a warp and stage;
 //  - a second producer brings the activation rows, so that weights can be under way before
 //    the activations they will meet have been computed;
