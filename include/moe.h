@@ -214,8 +214,8 @@ typedef enum {
 
 /* Activation quantisation.  Row r of x (bf16 or fp32, device) starts at x + r * ldx
  * elements and holds cols values v, or with gated = 1 cols values g and then cols values u,
- * and v = silu(g) * u in fp32.  For every group of 128 consecutive columns (the last one
- * may be shorter):
+ * and v = silu(g) * u with silu(g) = g / (1 + e^-g), in fp32.  For every group of 128
+ * consecutive columns (the last one may be shorter):
  *   scales[r, group] = amax / 448 over the group's |v| (fp32; 1 where that is 0)
  *   codes[r, c]      = the e4m3 value nearest v / scale (fp32 division, ties to even, at most
  *                      448: a subnormal scale is coarse)

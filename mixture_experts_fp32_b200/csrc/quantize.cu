@@ -93,14 +93,16 @@ __device__ __forceinline__ float2 quotient(float2 n, float s, float r) {
   return __ffma2_rn(__ffma2_rn(q1, s2, n), nr2, q1);
 }
 
-// silu(g) * u; the quotient of silu by the same method (d = 1 + e^-g >= 1; above 2^100 the
-// division itself).
+// silu(g) * u, silu's quotient g / d with d = 1 + e^-g by the same method, which needs a finite
+// quotient (of an infinite one the remainder is inf - inf) and a d that neither overflows nor
+// takes the remainder out of range; beyond |g| = 69, where d passes 2^99 or is 1, the division
+// itself.
 __device__ __forceinline__ float gated_value(float g, float u) {
   const float d = 1.0f + expf(-g);
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
   const float q = g * r;
-  return (d <= 0x1p100f ? fmaf(fmaf(-q, d, g), r, q) : g / d) * u;
+  return (fabsf(g) <= 69.f ? fmaf(fmaf(-q, d, g), r, q) : g / d) * u;
 }
 
 // IT: type of the group index (int where rows * groups allows it)
