@@ -93,16 +93,17 @@ __device__ __forceinline__ float2 quotient(float2 n, float s, float r) {
   return __ffma2_rn(__ffma2_rn(q1, s2, n), nr2, q1);
 }
 
-// silu(g) * u, silu's quotient g / d with d = 1 + e^-g by the same method, which needs a finite
-// quotient (of an infinite one the remainder is inf - inf) and a d that neither overflows nor
-// takes the remainder out of range; beyond |g| = 69, where d passes 2^99 or is 1, the division
-// itself.
-__device__ __forceinline__ float gated_value(float g, float u) {
-  const float d = 1.0f + expf(-g);
+// silu(g) * u from n = -g, silu's quotient g / d with d = 1 + e^-g by the same method, which needs
+// a finite quotient (of an infinite one the remainder is inf - inf) and a d that neither
+// overflows nor takes the remainder out of range; beyond |g| = 69, where d passes 2^99 or is 1,
+// the division itself.  Corrected by n + q d like the quotients of the codes: a quotient of -0
+// stays one.
+__device__ __forceinline__ float gated_value(float n, float u) {
+  const float d = 1.0f + expf(n);
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-  const float q = g * r;
-  return (fabsf(g) <= 69.f ? fmaf(fmaf(-q, d, g), r, q) : g / d) * u;
+  const float q = n * -r;
+  return (fabsf(n) <= 69.f ? fmaf(fmaf(q, d, n), -r, q) : -n / d) * u;
 }
 
 // IT: type of the group index (int where rows * groups allows it)
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(256, 4) quantize_groups_kernel(
       raw_up.negated(up);
 #pragma unroll
       for (int i = 0; i < kVals / 2; ++i)
-        v[i] = make_float2(gated_value(-v[i].x, up[i].x), gated_value(-v[i].y, up[i].y));
+        v[i] = make_float2(gated_value(v[i].x, up[i].x), gated_value(v[i].y, up[i].y));
       amax = Raw<XT>::largest(v);
     } else {
       amax = raw.amax();

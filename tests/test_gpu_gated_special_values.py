@@ -85,3 +85,20 @@ def test_large_gates():
     assert ((scales.double() - want).abs() <= 2.0 ** -20 * want).all()
     got = codes.view(E4M3).double() * scales.double()
     assert ((got - h).abs() <= (2.0 ** -4 + 2.0 ** -19) * h.abs() + 2.0 ** -10 * scales.double()).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_zeros_keep_their_sign(dtype):
+    """silu(-0) = -0 and a product's sign is that of its factors: codes 0x80 and 0x00, beside values
+    that make the scale ordinary and in a group of zeros."""
+    signs = [(-0.0, 1.0), (-0.0, -1.0), (0.0, 1.0), (0.0, -1.0), (2.0, -0.0), (-2.0, -0.0),
+             (2.0, 0.0), (-2.0, 0.0)]
+    want = torch.tensor([0x80, 0, 0, 0x80, 0x80, 0, 0, 0x80], dtype=torch.uint8)
+    g, u = ordinary(1)
+    for at in (16, 136):
+        g[0, at:at + 8] = torch.tensor([s[0] for s in signs])
+        u[0, at:at + 8] = torch.tensor([s[1] for s in signs])
+    g[0, 128:136], g[0, 144:] = 0.0, 0.0          # the second group: nothing but zeros
+    codes, scales = gated(g, u, dtype)
+    assert scales[0, 1] == 1.0 and scales[0, 0] != 1.0
+    assert torch.equal(codes[0, 16:24], want) and torch.equal(codes[0, 136:144], want)
