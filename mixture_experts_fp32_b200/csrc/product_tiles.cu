@@ -430,10 +430,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         mbar_wait_sleep_warp(smem_u32(&s.teardown), 0, kTeardownNs, p.status, kBit);
       }
-    } else if (warp == 1) {
-      // odd CTA: the pair's last MMAs before tensor memory is freed
-      if (pair < t.total)
-        mbar_wait_sleep_warp(smem_u32(&s.teardown), 0, kTeardownNs, p.status, kBit);
     }
     __syncwarp();
   } else {
@@ -584,6 +580,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // barriers or have the tensor core read its shared memory.
   tc_fence_before();
   __syncthreads();
+  // odd CTA: the pair's last commit arrives here too.  Not waited for before its roles have
+  // finished: a limit that ran from the launch on would bound the whole product.
+  if (warp == 1 && rank != 0 && pair < t.total)
+    mbar_wait_sleep_warp(smem_u32(&s.teardown), 0, kTeardownNs, p.status, kBit);
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
