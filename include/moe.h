@@ -183,7 +183,8 @@ moe_status moe_forward(moe_plan_t plan, const moe_weights *weights, const void *
  * one read of the selected experts' weights; the same layer, arguments, weights and
  * workspace as moe_forward, with the same rules for ties, padding rows and rounding, so
  * the two agree to the rounding of their sums (which they take in other orders; bf16
- * weights: h enters the down product with about fp32's precision in both; FP8: the y of
+ * weights: h enters the down product as two bf16 parts, 16 bits of fraction, in both, and
+ * an infinite h, NaN in moe_forward's result, is infinite in this one's; FP8: the y of
  * an expert is not rounded to bf16 before the combine here).  Each expert weight is read
  * once per call whatever the number of tokens that selected it; experts that no token
  * selected are not read.
