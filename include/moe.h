@@ -225,8 +225,9 @@ typedef enum {
  * their codes are 0 and their scales 1, so a product with them gives zero rows.  A NaN
  * gives NaN codes where it stands and is left out of its group's amax; an infinite
  * amax gives code 0 to the group's finite values and NaN to the infinite ones.
- * cols is a multiple of 16 (else MOE_ERR_UNSUPPORTED); ldx >= cols * (1 + gated), with rows
- * of x and codes 16-byte aligned (ldx a multiple of 8 for bf16, of 4 for fp32).
+ * cols is a multiple of 16, at most 2^31 - 128 (else MOE_ERR_UNSUPPORTED); ldx >=
+ * cols * (1 + gated), with rows of x and codes 16-byte aligned (ldx a multiple of 8 for
+ * bf16, of 4 for fp32).
  * Needs no workspace; x must not overlap codes or scales. */
 moe_status moe_quantize_groups(const void *x, moe_dtype x_type, int rows, int cols, int64_t ldx,
                                int gated, const uint8_t *valid, void *codes, float *scales,

@@ -208,7 +208,8 @@ MOE_EXPORT moe_status moe_quantize_groups(const void* x, moe_dtype x_type, int r
                                           void* codes, float* scales, void* stream) {
   if (rows < 0 || cols < 1 || (gated != 0 && gated != 1)) return MOE_ERR_INVALID_ARG;
   if (x_type != MOE_T_BF16 && x_type != MOE_T_FP32) return MOE_ERR_INVALID_ARG;
-  if (cols % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  // the groups' columns are reckoned in int
+  if (cols % 16 != 0 || cols > 0x7fffffff - 127) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   const int64_t width = (int64_t)cols * (gated ? 2 : 1);
   const int64_t per16 = x_type == MOE_T_BF16 ? 8 : 4;
