@@ -92,7 +92,8 @@ typedef struct moe_plan_s *moe_plan_t;
 
 /* Validates the shape and sizes the workspace.  Host only: touches no device.
  * *plan receives a new plan (free with moe_plan_destroy), *workspace_bytes the
- * device workspace size every forward with this plan needs. */
+ * device workspace size with which every call of this plan runs (moe_forward_few's
+ * memory is that of the other forwards: the size is the larger of the two). */
 moe_status moe_plan_create(const moe_config *cfg, moe_plan_t *plan, size_t *workspace_bytes);
 void moe_plan_destroy(moe_plan_t plan);
 
@@ -412,7 +413,8 @@ moe_status moe_check_device_status(moe_plan_t plan, void *workspace, void *strea
                                    uint32_t *bits);
 
 /* Device addresses of the intermediate buffers inside a workspace, for
- * inspection after a forward (host arithmetic only; nothing is launched):
+ * inspection after a forward (host arithmetic only; nothing is launched; not after
+ * moe_forward_few, which uses the memory for buffers of its own):
  *  row_token  int32 [R]     token index of each permuted row (R = Tv*(k+S))
  *  x_perm     [R, H]        permuted activations (bf16; e4m3 codes for FP8)
  *  h          SwiGLU output rows: bf16 weights: [2R, Imax], row 2r = bf16(h_r) and

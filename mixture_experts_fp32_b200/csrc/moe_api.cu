@@ -21,9 +21,10 @@ struct moe_plan_s {
   size_t off_status, off_goff, off_done, off_wsplit, off_rscratch, off_partial, off_logits,
       off_ids, off_w, off_perm,
       off_inv, off_rowtok, off_xp, off_sx, off_h, off_sh, off_y;
-  // moe_forward_few
-  size_t off_few_logits, off_few_part, off_few_h, off_few_sh;
+  // moe_forward_few, in the memory behind the status word that the other forwards' regions take
+  size_t off_few_logits, off_few_part, off_few_xq, off_few_sx, off_few_h, off_few_sh;
   int few_slots;
+  size_t forward_bytes, few_bytes;     // what either needs; ws_bytes is the larger
   unsigned long long wait_limit_ns;
   int device;
   int num_sms;
@@ -68,14 +69,14 @@ void record(moe_debug* dbg, int i, cudaStream_t st) {
 }
 
 moe_status check_common(const moe_plan_s* p, int T, int k, const void* workspace,
-                        size_t ws_bytes) {
+                        size_t ws_bytes, bool few = false) {
   if (p == nullptr) return MOE_ERR_INVALID_ARG;
   if (T < 0 || T > p->cfg.max_tokens) return MOE_ERR_INVALID_ARG;
   if (k < 1 || k > p->cfg.top_k_max) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
     return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < p->ws_bytes) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < (few ? p->few_bytes : p->forward_bytes)) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
 
@@ -202,20 +203,25 @@ MOE_EXPORT moe_status moe_plan_create(const moe_config* cfg, moe_plan_t* plan,
     p->off_sh = take(sizeof(float) * ((size_t)imax / 128) * r_cap);
     p->off_y = take(2 * r_cap * H);
   }
-  // moe_forward_few: router sums, counters, partial tiles, h in rows [slot][token] (bf16: two
-  // parts; FP8: codes and scales)
+  p->forward_bytes = off;
+  // moe_forward_few: router sums, partial tiles, x (FP8: codes and scales), h in rows
+  // [slot][token] (bf16: two parts; FP8: codes and scales).  No call leaves anything there for the
+  // next one, so these lie where the regions above do, but for the status word.
   const size_t few = T < MOE_FEW_TOKENS_MAX ? T : MOE_FEW_TOKENS_MAX;
   const size_t slots = (E < few * c.top_k_max ? E : few * c.top_k_max) + S;
   const size_t few_rows = slots * MOE_FEW_TOKENS_MAX;
+  const bool few_fp8 = c.wtype != MOE_W_BF16;
   p->few_slots = (int)slots;
+  off = p->off_goff;
   p->off_few_logits =
       take(sizeof(float) * moe::kFewRouterSplits * MOE_FEW_TOKENS_MAX * E);
-  p->off_few_part =
-      take(sizeof(float) * moe::kWsCtas * 4 * MOE_FEW_TOKENS_MAX * moe::kWsRows);
-  const bool few_fp8 = c.wtype != MOE_W_BF16;
+  p->off_few_part = take(sizeof(float) * moe::kWsCtas * 4 * few * moe::kWsRows);
+  p->off_few_xq = few_fp8 ? take(few * H) : 0;
+  p->off_few_sx = few_fp8 ? take(sizeof(float) * few * (H / 128)) : 0;
   p->off_few_h = take(few_rows * (size_t)imax * (few_fp8 ? 1 : 4));
   p->off_few_sh = few_fp8 ? take(sizeof(float) * few_rows * (imax / 128)) : 0;
-  p->ws_bytes = off;
+  p->few_bytes = off;
+  p->ws_bytes = p->few_bytes > p->forward_bytes ? p->few_bytes : p->forward_bytes;
   p->wait_limit_ns = 2000000000ull;
   p->device = -1;
   p->num_sms = 0;
@@ -515,7 +521,7 @@ MOE_EXPORT moe_status moe_forward_few(moe_plan_t plan, const moe_weights* wts, c
                                       const uint8_t* valid, int T, int k, void* out,
                                       void* workspace, size_t ws_bytes, void* stream,
                                       moe_debug* dbg) {
-  moe_status s = check_common(plan, T, k, workspace, ws_bytes);
+  moe_status s = check_common(plan, T, k, workspace, ws_bytes, true);
   if (s != MOE_OK) return s;
   if (wts == nullptr) return MOE_ERR_INVALID_ARG;
   if (T > MOE_FEW_TOKENS_MAX) return MOE_ERR_UNSUPPORTED;
@@ -556,8 +562,8 @@ MOE_EXPORT moe_status moe_forward_few(moe_plan_t plan, const moe_weights* wts, c
   a.h_slots = plan->few_slots;
   a.h = at<uint8_t>(workspace, plan->off_few_h);
   a.sh = at<float>(workspace, plan->off_few_sh);
-  a.xq = at<uint8_t>(workspace, plan->off_xp);
-  a.sx = at<float>(workspace, plan->off_sx);
+  a.xq = at<uint8_t>(workspace, plan->off_few_xq);
+  a.sx = at<float>(workspace, plan->off_few_sx);
   a.part = at<float>(workspace, plan->off_few_part);
   a.status = at<unsigned int>(workspace, plan->off_status);
   a.bar = a.status + 16;               // beside the status word, cleared with it
