@@ -56,7 +56,7 @@ moe_status ensure_device(moe_plan_s* p) {
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   if (p->device == dev) return MOE_OK;
   int sms = 0;
-  const moe_status s = moe::check_device(&sms, &dev);
+  const moe_status s = moe::check_device(moe::KernelSet::kLayer, &sms, &dev);
   if (s != MOE_OK) return s;
   p->num_sms = sms;
   p->device = dev;
@@ -86,30 +86,41 @@ namespace moe {
 
 moe_status cuda_status(cudaError_t e) { return check_launch(e); }
 
-moe_status check_device(int* num_sms, int* device) {
+moe_status check_device(KernelSet set, int* num_sms, int* device) {
   constexpr int kMaxDevices = 64;
+  struct Device {
+    int sms = 0;                                     // 0: not looked at yet
+    bool ready[(int)KernelSet::kNone] = {};
+  };
   static std::mutex mu;
-  static int sms_of[kMaxDevices];      // 0: not prepared yet
+  static Device devices[kMaxDevices];
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return MOE_ERR_CUDA;
   if (dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
   std::lock_guard<std::mutex> lock(mu);
-  if (sms_of[dev] == 0) {
+  Device& d = devices[dev];
+  if (d.sms == 0) {
     int sms = 0, major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return MOE_ERR_CUDA;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
     if (major != 10 || minor != 0) return MOE_ERR_UNSUPPORTED;   // built for sm_100a only
-    if (check_launch(prepare_grouped_gemm_kernels()) != MOE_OK ||
-        check_launch(prepare_grouped_gemm_fp8_kernels()) != MOE_OK ||
-        check_launch(prepare_router_kernel()) != MOE_OK ||
-        check_launch(prepare_few_kernels()) != MOE_OK ||
-        check_launch(prepare_product_kernels()) != MOE_OK)
-      return MOE_ERR_CUDA;
-    sms_of[dev] = sms;
+    d.sms = sms;
   }
-  if (num_sms != nullptr) *num_sms = sms_of[dev];
+  if (set != KernelSet::kNone && !d.ready[(int)set]) {
+    cudaError_t e = cudaSuccess;
+    if (set == KernelSet::kLayer) {
+      e = prepare_grouped_gemm_kernels();
+      if (e == cudaSuccess) e = prepare_grouped_gemm_fp8_kernels();
+      if (e == cudaSuccess) e = prepare_router_kernel();
+    } else {
+      e = set == KernelSet::kFew ? prepare_few_kernels() : prepare_product_kernels();
+    }
+    if (e != cudaSuccess) return check_launch(e);
+    d.ready[(int)set] = true;
+  }
+  if (num_sms != nullptr) *num_sms = d.sms;
   if (device != nullptr) *device = dev;
   return MOE_OK;
 }
@@ -531,7 +542,8 @@ MOE_EXPORT moe_status moe_forward_few(moe_plan_t plan, const moe_weights* wts, c
   if (out == nullptr || !aligned16(out)) return MOE_ERR_INVALID_ARG;
   const moe_config& c = plan->cfg;
   if ((s = check_weights(c, wts, hidden)) != MOE_OK) return s;
-  if ((s = ensure_device(plan)) != MOE_OK) return s;
+  int sms = 0;
+  if ((s = moe::check_device(moe::KernelSet::kFew, &sms)) != MOE_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool fp8 = c.wtype == MOE_W_FP8_E4M3_B128;
   moe::FewArgs a;
@@ -577,7 +589,7 @@ MOE_EXPORT moe_status moe_forward_few(moe_plan_t plan, const moe_weights* wts, c
   record(dbg, 0, st);
   s = check_launch(cudaMemsetAsync(a.status, 0, kAlign, st));
   if (s != MOE_OK) return s;
-  s = check_launch(moe::launch_few(a, fp8, plan->num_sms, st));
+  s = check_launch(moe::launch_few(a, fp8, sms, st));
   if (s != MOE_OK) return s;
   record(dbg, MOE_NUM_STAGES, st);
   return MOE_OK;

@@ -192,8 +192,10 @@ cudaError_t prepare_few_kernels();
 cudaError_t prepare_product_kernels();
 
 // Entry points' common parts (moe_api.cu).
-// The current device: sets the kernels' attributes on its first use, counts its SMs.
-moe_status check_device(int* num_sms = nullptr, int* device = nullptr);
+// The current device: on their first use there, sets the attributes of the kernels that a call takes
+// (one set refused leaves the others usable); counts its SMs.
+enum class KernelSet { kLayer, kFew, kProduct, kNone };
+moe_status check_device(KernelSet set, int* num_sms = nullptr, int* device = nullptr);
 // MOE_OK, or MOE_ERR_CUDA with the error kept for moe_last_cuda_error_string.
 moe_status cuda_status(cudaError_t e);
 moe_status read_device_status(unsigned int* status, cudaStream_t st, uint32_t* bits);

@@ -212,7 +212,7 @@ MOE_EXPORT moe_status moe_block_scaled_product(moe_product_t p, const void* a,
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < p->ws_bytes) return MOE_ERR_WORKSPACE;
   int sms = 0;
-  moe_status s = moe::check_device(&sms);
+  moe_status s = moe::check_device(moe::KernelSet::kProduct, &sms);
   if (s != MOE_OK) return s;
   auto* st = static_cast<cudaStream_t>(stream);
   auto* ws = static_cast<uint8_t*>(workspace);

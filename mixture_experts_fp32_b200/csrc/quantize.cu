@@ -217,7 +217,7 @@ MOE_EXPORT moe_status moe_quantize_groups(const void* x, moe_dtype x_type, int r
       (reinterpret_cast<uintptr_t>(x) & 15u) != 0 || (reinterpret_cast<uintptr_t>(codes) & 15u) != 0 ||
       (reinterpret_cast<uintptr_t>(scales) & 3u) != 0)
     return MOE_ERR_INVALID_ARG;
-  moe_status s = moe::check_device();
+  moe_status s = moe::check_device(moe::KernelSet::kNone);
   if (s != MOE_OK) return s;
   auto* st = static_cast<cudaStream_t>(stream);
   return moe::cuda_status(
