@@ -223,7 +223,8 @@ def _addr(t, name: str = "argument", dtypes=None) -> int | None:
     return t.data_ptr()
 
 
-def _stream(s) -> int | None:
+def _stream(s, device: int | None = None) -> int | None:
+    """The handle of a stream, by default the current one of ``device`` (None: the current)."""
     if s is None:
         import torch
         # the current stream's handle without a Stream object around it, 3.5 us less a call (a
@@ -231,7 +232,7 @@ def _stream(s) -> int | None:
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is None:
             return torch.cuda.current_stream().cuda_stream
-        return raw(torch.cuda.current_device())
+        return raw(torch.cuda.current_device() if device is None else device)
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -370,13 +371,14 @@ def moe_forward_few(plan, weights: moe_weights, hidden, valid, T: int, k: int, o
     _check(st, "moe_forward_few")
 
 
-def _on_current_device(tensors) -> None:
-    """Every tensor on the current device: the library launches there."""
+def _on_current_device(tensors) -> int:
+    """Every tensor on the current device, whose index is returned: the library launches there."""
     import torch
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != cur:
+        if t is not None and t.get_device() != cur and t.is_cuda:
             raise ValueError(f"a tensor on {t.device}, while the current device is cuda:{cur}")
+    return cur
 
 
 def _rows_of(t, name: str, dtypes) -> tuple[int, int]:
@@ -417,9 +419,10 @@ def moe_quantize_groups(x, codes, scales, valid=None, gated: bool = False, strea
     addr, ld = _rows_of(x, "x", _BF16 + _F32)
     c, s, v = (_addr(codes, "codes", _CODES), _addr(scales, "scales", _F32),
                _addr(valid, "valid", _MASK))
-    _on_current_device((x, codes, scales, valid))
+    device = _on_current_device((x, codes, scales, valid))
     _check(load().moe_quantize_groups(addr, MOE_T_FP32 if x.element_size() == 4 else MOE_T_BF16,
-                                      rows, cols, ld, int(bool(gated)), v, c, s, _stream(stream)),
+                                      rows, cols, ld, int(bool(gated)), v, c, s,
+                                      _stream(stream, device)),
            "moe_quantize_groups")
 
 
