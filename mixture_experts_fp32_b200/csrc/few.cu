@@ -31,10 +31,14 @@
 // by the shapes and the routing.
 //
 // Measured: one token through 3 of 48 experts and the shared one (882 MB of bf16 weights) in
-// 142 us, 6200 GB/s; through 8 of 256 and the shared one (404 MB of e4m3) in 79 us, 5100 GB/s;
-// 13 tokens through 35 of 40 small experts (119 MB) in 38 us, of which 18 are the weights',
-// 8 the router and selection, and the rest the meetings and the first loads after them.
-// Nothing but those: 16 tokens through 8 experts of 200 KB take 25 us.
+// 144 us, 6100 GB/s; through 8 of 256 and the shared one (404 MB of e4m3) in 78 us, 5200 GB/s;
+// 16 rows of a padded batch through 46 experts and the shared one (4.1 GB of bf16) in 640 us,
+// 6500 GB/s.  These are after a rest, called or replayed alike; under lasting load the card's
+// power limit takes clocks from 1965 to 1170-1580 MHz, and they take 160, 86 and 740 us.
+// 13 rows, 11 of them tokens, through 15 of 40 small experts and the shared one (61 MB of
+// e4m3, 9.3 us at HBM's rate) in 37 us: 8 are the router and selection, 6 the second meeting
+// and the first h after it, 4 the last tiles; both phases stream in the other 19, of which bytes
+// account for 9.  Nothing but latencies: 16 tokens through 8 experts of 200 KB take 25 us.
 #include <cudaTypedefs.h>
 
 #include "weight_stream.cuh"

@@ -134,8 +134,13 @@ cudaError_t launch_rows(const ProductArgs& a, int ctas, cudaStream_t st) {
 
 // Whether row blocks of 32 are quicker than 256-row tiles: a stage of the stream (256 features of a
 // block against 128 K) takes a CTA 900 clocks, the meeting of the CTAs 5000 more than the end
-// of a tile, and the tiles what product_tiles.cu reckons (64 rows of 4096 x 7168: 16.3 us as
-// blocks, 20.1 as tiles; 77 of 1111 x 1200: 12.5 and 20.5; 128 of 7168 x 2048: 18.6 and 16.5).
+// of a tile, and the tiles what product_tiles.cu reckons.  Replayed from a graph, as decode
+// runs them: 64 rows of 4096 x 7168 16.5 us as blocks, 19.9 as tiles; 77 of 1111 x 1200 12.7
+// and 18.5; 128 of 7168 x 2048 18.5 and 16.4.  Called one after another, where blocks pay their
+// memset and cooperative launch in full: 20.6 and 20.6, 16.5 and 20.3, 22.6 and 16.7.  Of 75
+// sizes replayed (40 to 128 rows) the rule missed the quicker form in 3, by 6 % at most.
+// Units are divided by all CTAs although small work goes to fewer (WsSplit): with the units
+// that these really take it missed 7, four of them by 40 to 50 %.
 bool rows_are_few(const ProductArgs& p, int ctas, int num_sms) {
   if (p.M <= kProductRows) return true;
   if (p.M > kProductBlocks * kProductRows) return false;

@@ -21,7 +21,7 @@ struct ProductArgs {
   int M, N, K, kb;                             // kb: blocks of 128 K
   bool f32;
   float* part;                                 // partial sums of split tiles
-  unsigned int* counters;                      // zero before and after a launch
+  unsigned int* counters;                      // zeroed before a launch, which leaves its parts' count
   unsigned int* status;
   unsigned long long wait_limit_ns;
 };

@@ -543,11 +543,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
+std::atomic<int> resident_pairs{kProductPairs};       // clusters a device holds at once, at most
+
 // The register shares of the warpgroups only add up if the kernel was built with exactly
 // kLaunchRegs registers a thread; anything else is refused rather than launched (a
 // mismatched split would wait forever).
-std::atomic<int> resident_pairs{kProductPairs};       // clusters a device holds at once, at most
-
 template <bool F32>
 cudaError_t prepare() {
   static_assert(sizeof(TileSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");

@@ -10,8 +10,8 @@
 // two codes), but sixteen divisions a lane cost more than the bytes.  They take one
 // reciprocal a lane and four fused multiply-adds a value instead (quotient below), two values
 // an instruction; the next group's loads are on their way meanwhile.  Instructions still bound
-// it more than bytes (7168 columns of 8192 rows of bf16: 42 us, 4200 GB/s; one group at a time
-// with divisions 51 us).  Registers are held to 64, so that four blocks share an SM: gated
+// it more than bytes (7168 columns of 8192 rows of bf16: 41 us, 4350 GB/s, 64 % of issue slots;
+// one group at a time with divisions 51 us).  Registers are held to 64, so that four blocks share an SM: gated
 // values spill a little and are faster for it (fp32, 4099 rows of 2 x 2064, 900 of them
 // padding: 19 against 21 us), the others 42 against 46.
 #include "moe_internal.cuh"

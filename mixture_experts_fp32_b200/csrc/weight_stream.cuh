@@ -1,10 +1,12 @@
 // Streaming a weight matrix past a few activation rows: the pieces shared by the
 // few-token layer and the block-scaled product of few rows.
 //
-// Both read every weight once and multiply it with 32 activation rows at most, so they are
-// bound by HBM, not by arithmetic: at 6.5 TB/s an SM receives about 23 bytes of weights a
-// clock, 256 rows x 128 bytes of K every 1400 clocks.  What matters is that nothing else
-// takes longer than that, and that loads never pause:
+// Every weight comes from HBM once and meets 32 activation rows at most, so both are bound by
+// HBM, not by arithmetic: at 6.5 TB/s an SM receives about 23 bytes of weights a clock, 256
+// rows x 128 bytes of K every 1400 clocks.  (A product of 33 to 128 rows is two to four blocks of
+// 32 of them: these bring the weights to shared memory once each, after the first from L2, and
+// share its rate.)  What matters is that nothing else takes longer than that, and that loads
+// never pause:
 //  - weights travel by TMA into a ring of stages in shared memory (256 weight rows x 128
 //    bytes of K, two boxes of 128 rows), 160 KB or more a CTA in flight, by a producer that
 //    runs on across tiles, barriers and phases;
